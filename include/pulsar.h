@@ -55,7 +55,8 @@ typedef enum {
   PA_ERR_WORKSPACE = -3,   /* ws NULL, misaligned, or smaller than *_workspace_size() */
   PA_ERR_CUDA = -4,        /* a CUDA launch or memset failed */
   PA_ERR_TIMEOUT = -5,     /* a bounded device-side wait expired (device status only) */
-  PA_ERR_RANGE = -6        /* a value left the range of an internal format (device status only) */
+  PA_ERR_RANGE = -6,       /* a value left the range of an internal format (device status only) */
+  PA_ERR_CAPACITY = -7     /* a page pool or page table is too small (device status only) */
 } pa_status;
 
 typedef enum { PA_F32 = 0, PA_BF16 = 1 } pa_dtype;

@@ -214,6 +214,7 @@ const char* pa_status_string(int status) {
     case PA_ERR_CUDA: return "CUDA launch or copy failed";
     case PA_ERR_TIMEOUT: return "bounded device wait expired";
     case PA_ERR_RANGE: return "value outside the internal fp16 range";
+    case PA_ERR_CAPACITY: return "page pool or page table too small";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,177 @@
+// Internal interface of the serving operators (include/pulsar_serving.h):
+// kernel arguments, the work plan of an attention call and the launchers.
+#pragma once
+
+#include "pa_internal.h"
+#include "../../include/pulsar_serving.h"
+
+namespace pa {
+
+constexpr int kMaxRequests = 8192;   // prefix sums of a step are staged in shared memory
+constexpr int kMaxGroup = 64;        // query heads per kv head: a tile holds at least one token
+constexpr int kSms = 148;
+constexpr int kPlanTile = 128;       // keys per unit of planned work
+
+struct ScheduleArgs {
+  const int32_t *q_len, *kv_len;
+  int32_t B;
+  int32_t* block_table;
+  int64_t table_stride;
+  int32_t max_pages;
+  const int32_t* free_pages;
+  int32_t n_free, page_size;
+  int64_t n_tokens;
+  int32_t *cu_q, *kv_len_out, *positions, *slots, *n_used;
+  DeviceStatus* status;
+};
+int launch_paged_schedule(const ScheduleArgs& a, cudaStream_t s);
+
+struct AppendArgs {
+  const void *q, *k, *v;
+  int dtype;
+  int64_t N, ldq, ldk, ldv;
+  int32_t hq, hkv, d;
+  double rope_theta;
+  const int32_t *positions, *slots;
+  void *k_pages, *v_pages;
+  int64_t n_slots;
+  void *q_out, *k_out;
+  DeviceStatus* status;
+};
+int launch_paged_append(const AppendArgs& a, cudaStream_t s);
+
+// One unit of attention work: the rows of up to `tokens` new tokens of a
+// request (all query heads of one kv head) against key tiles [kt0, kt1).
+struct Piece {
+  int32_t b, tok0;    // request, first of its new tokens
+  int32_t kt0, kt1;   // key tiles of kPlanTile keys
+  int32_t part;       // slot of its partial result, or -1: it has all the keys
+  int32_t row0;       // cu_q[b]
+  int32_t q_len, kv_len;
+};
+static_assert(sizeof(Piece) == 32, "a piece is two 16-byte loads");
+
+// Rows whose keys were cut into several pieces (merged afterwards).
+struct MergeItem {
+  int32_t row0, n_tok;      // first packed row, tokens
+  int32_t part0, n_parts;
+};
+
+// Start of one block's range of decode work: request, kv head and key group
+// of its first unit, and the units in all.
+struct DecodeStart {
+  int32_t b, kvh, unit, pad;
+};
+
+struct PlanHead {
+  int32_t n_pieces;     // pieces of the tile kernels, per kv head
+  int32_t n_items;      // entries of the merge list
+  int32_t abort;        // a bounded wait ran out somewhere
+  int32_t pad;
+  int64_t decode_units; // key groups of the decode kernel, over kv heads
+};
+
+struct AttendArgs {
+  int dtype;
+  const void *q, *k, *v;          // k, v: packed rows or pages
+  int64_t N, ldq, ldk, ldv;       // ldk, ldv: packed rows only
+  const int32_t* cu_q;
+  const int32_t* kv_len;          // null: prompts (kv_len = q_len)
+  int32_t B, max_q;
+  const int32_t* block_table;     // null: packed rows
+  int64_t table_stride;
+  int32_t max_pages, page_size, page_shift;
+  int64_t n_slots;                // rows of k, v
+  int32_t hq, hkv, d;
+  void* o;
+  float* lse;
+  // ------------------------------------------------ plan (serving_plan.cu)
+  int32_t tile_tokens;            // new tokens per piece
+  int32_t tile_rows;              // rows a partial result has room for
+  int32_t small_rows;             // requests of at most so many rows go to the decode kernel
+  int32_t piece_cap;              // pieces the workspace has room for
+  int32_t part_cap;               // partial results it has room for, per kv head; 0: never cut
+  int32_t item_cap;
+  int32_t decode_ctas;            // 0: no decode kernel
+  DeviceStatus* status;
+  PlanHead* head;
+  Piece* pieces;
+  MergeItem* items;
+  DecodeStart* starts;            // [decode_ctas]
+  int32_t* done;                  // [decode_ctas] arrivals at a cut (request, kv head)
+  float* part_o;                  // [part_cap][hkv][tile_rows][d]
+  float* part_lse;                // [part_cap][hkv][tile_rows]
+  float* dec_o;                   // [2 * decode_ctas][16][d]
+  float* dec_lse;                 // [2 * decode_ctas][16]
+  uint64_t wait_limit_ns = 1000000000ull;
+};
+// Fills the plan's sizes and returns the workspace bytes; with `ws` set,
+// carves it.  `max_kv` is the longest cache a request may have.
+size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws);
+int launch_attend(const AttendArgs& a, cudaStream_t s);
+
+int launch_attend_simt(const AttendArgs& a, cudaStream_t s);
+
+// keys of a request that the first `n` of its new tokens see
+__host__ __device__ inline int64_t keys_seen(int64_t kv_len, int64_t q_len, int64_t n) {
+  const int64_t k = kv_len - q_len + n;
+  return k < 0 ? 0 : k;
+}
+
+#ifdef __CUDACC__
+// Slot of key `key` of request b, or -1 (recorded) when its page is not in
+// the cache.
+__device__ __forceinline__ int64_t key_slot(const AttendArgs& a, int b, int64_t key) {
+  const int page = a.block_table[static_cast<int64_t>(b) * a.table_stride + (key >> a.page_shift)];
+  const int64_t slot = (static_cast<int64_t>(page) << a.page_shift) + (key & (a.page_size - 1));
+  if (page < 0 || slot >= a.n_slots) {
+    set_status(a.status, PA_ERR_INVALID, b, page);
+    return -1;
+  }
+  return slot;
+}
+
+template <typename T>
+__device__ __forceinline__ T warp_incl_scan(T x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Inclusive scan over a block of 1024 threads; *total receives the sum.
+// `tmp` has 33 elements; every thread of the block calls it.
+template <typename T>
+__device__ __forceinline__ T block_incl_scan(T x, T* tmp, T* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  x = warp_incl_scan(x);
+  if (lane == 31) tmp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    const T w = warp_incl_scan(tmp[lane]);
+    tmp[lane] = w;
+  }
+  __syncthreads();
+  const T before = warp > 0 ? tmp[warp - 1] : T(0);
+  *total = tmp[31];
+  __syncthreads();
+  return before + x;
+}
+
+// Largest i in [0, n) with pre[i] <= x (pre[0] <= x; pre non-decreasing).
+template <typename T>
+__device__ __forceinline__ int upper_index(const T* pre, int n, T x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+#endif
+
+}  // namespace pa

@@ -1,0 +1,218 @@
+// The page tables and slot map of a serving step, and the rotation of its
+// new tokens with their append to the paged cache.
+#include <cmath>
+
+#include "serving.h"
+
+namespace pa {
+
+namespace {
+
+__device__ __forceinline__ int32_t sat32(int64_t x) {
+  return static_cast<int32_t>(x < INT32_MAX ? x : INT32_MAX);
+}
+
+// What request b asks for: its lengths, the pages it holds and needs.
+struct Request {
+  int64_t q, kv;
+  int64_t held, need;
+  bool fits, bad;
+};
+
+__device__ __forceinline__ Request request_of(const ScheduleArgs& a, int b) {
+  Request r;
+  r.q = a.q_len[b];
+  r.kv = a.kv_len[b];
+  r.bad = r.q < 0 || r.kv < 0;
+  if (r.q < 0) r.q = 0;
+  if (r.kv < 0) r.kv = 0;
+  r.held = (r.kv + a.page_size - 1) / a.page_size;
+  const int64_t all = (r.kv + r.q + a.page_size - 1) / a.page_size;
+  r.need = r.q > 0 ? all - r.held : 0;
+  r.fits = r.q == 0 || all <= a.max_pages;
+  return r;
+}
+
+// Two prefix sums over the requests (new tokens, new pages), then one entry
+// per token and per new page, each found by bisection in them.  Every block
+// builds the sums by itself (B is at most 8192: a few microseconds of loads
+// that hit L2), which saves a second launch and a grid-wide wait; tokens and
+// pages are spread over the blocks.
+__global__ void __launch_bounds__(1024) paged_schedule_kernel(ScheduleArgs a) {
+  extern __shared__ int32_t sm[];
+  int32_t* cu = sm;                  // [B + 1]
+  int32_t* pages = sm + a.B + 1;     // [B + 1] pages asked for before request b
+  __shared__ int64_t tmp[33];
+  __shared__ int32_t used;
+  if (threadIdx.x == 0) {
+    cu[0] = 0;
+    pages[0] = 0;
+    used = 0;
+  }
+  __syncthreads();
+  const bool first = blockIdx.x == 0;
+  int64_t tok_base = 0, page_base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 1024) {
+    const int b = b0 + threadIdx.x;
+    Request r = {};
+    r.fits = true;
+    if (b < a.B) r = request_of(a, b);
+    int64_t tok_all, page_all;
+    const int64_t toks = tok_base + block_incl_scan<int64_t>(r.q, tmp, &tok_all);
+    const int64_t pgs = page_base + block_incl_scan<int64_t>(r.fits ? r.need : 0, tmp, &page_all);
+    if (b < a.B) {
+      cu[b + 1] = sat32(toks);
+      pages[b + 1] = sat32(pgs);
+      const bool granted = r.fits && (r.need == 0 || pgs <= a.n_free);
+      if (granted && r.need > 0) atomicMax(&used, sat32(pgs));
+      if (first) {
+        a.cu_q[b + 1] = sat32(toks);
+        a.kv_len_out[b] = sat32(granted ? r.kv + r.q : r.kv);
+        if (r.bad) set_status(a.status, PA_ERR_INVALID, b);
+        else if (!granted) set_status(a.status, PA_ERR_CAPACITY, b);
+      }
+    }
+    tok_base += tok_all;
+    page_base += page_all;
+  }
+  __syncthreads();
+  if (first && threadIdx.x == 0) {
+    a.cu_q[0] = 0;
+    *a.n_used = used;
+    if (tok_base > a.n_tokens) set_status(a.status, PA_ERR_INVALID, a.B);
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 1024;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 1024 + threadIdx.x;
+  // the new pages into their requests' rows
+  for (int64_t x = id; x < used; x += step) {
+    const int b = upper_index(pages, a.B + 1, static_cast<int32_t>(x));
+    const Request r = request_of(a, b);
+    a.block_table[b * a.table_stride + r.held + (x - pages[b])] = a.free_pages[x];
+  }
+  // a position and a slot for each token
+  for (int64_t t = id; t < a.n_tokens; t += step) {
+    int32_t pos = 0, slot = -1;
+    if (t < cu[a.B]) {
+      const int b = upper_index(cu, a.B + 1, static_cast<int32_t>(t));
+      const Request r = request_of(a, b);
+      const int64_t p = r.kv + (t - cu[b]);
+      pos = sat32(p);
+      if (r.fits && (r.need == 0 || pages[b + 1] <= a.n_free)) {
+        const int64_t i = p / a.page_size;
+        const int64_t page = i < r.held ? a.block_table[b * a.table_stride + i]
+                                        : a.free_pages[pages[b] + (i - r.held)];
+        const int64_t s = page * a.page_size + p % a.page_size;
+        if (page < 0 || s > INT32_MAX) set_status(a.status, PA_ERR_INVALID, b, static_cast<int>(page));
+        else slot = static_cast<int32_t>(s);
+      }
+    }
+    a.positions[t] = pos;
+    a.slots[t] = slot;
+  }
+}
+
+// RoPE and append.  HBM-bound: each element is read once and written once,
+// in 16-byte accesses.  A block takes `tpb` tokens; the angles of a token
+// are computed once (fp64 product and reduction to one turn, fp32 sine and
+// cosine of the rest) and shared by its heads through shared memory.
+template <typename T>
+__global__ void __launch_bounds__(256) paged_append_kernel(AppendArgs a, RopeFreqs turns, int tpb) {
+  constexpr int V = 16 / sizeof(T);            // elements per access
+  extern __shared__ float2 cs[];               // [tpb][d / 2] (cos, sin)
+  const int half = a.d / 2;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tpb;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(tpb), a.N - t0));
+  const bool rope = a.rope_theta != 0.0;
+  if (rope) {
+    for (int e = threadIdx.x; e < nt * half; e += 256) {
+      const double x = a.positions[t0 + e / half] * turns.omega[e % half];   // angle in turns
+      const float f = static_cast<float>(x - rint(x));                       // in [-1/2, 1/2]
+      float sn, cn;
+      sincospif(2.f * f, &sn, &cn);
+      cs[e] = make_float2(cn, sn);
+    }
+    __syncthreads();
+  }
+  const int cpr = half / V;                    // accesses per half row
+  const int hq = a.q ? a.hq : 0;
+  const int hv = a.slots ? a.hkv : 0;
+  const int per_tok = (hq + a.hkv + hv) * cpr;
+  for (int e = threadIdx.x; e < nt * per_tok; e += 256) {
+    const int t = e / per_tok, i = e % per_tok;
+    const int head = i / cpr, m = (i % cpr) * V;
+    const int64_t tok = t0 + t;
+    int64_t slot = a.slots ? a.slots[tok] : -1;
+    if (slot >= a.n_slots) {
+      if (i == 0) set_status(a.status, PA_ERR_INVALID, static_cast<int>(tok), static_cast<int>(slot));
+      slot = -1;
+    }
+    const T* src;
+    T *dst, *page = nullptr;
+    if (head < hq) {
+      src = static_cast<const T*>(a.q) + tok * a.ldq + head * a.d;
+      dst = static_cast<T*>(a.q_out) + (tok * a.hq + head) * a.d;
+    } else if (head < hq + a.hkv) {
+      const int h = head - hq;
+      src = static_cast<const T*>(a.k) + tok * a.ldk + h * a.d;
+      dst = a.k_out ? static_cast<T*>(a.k_out) + (tok * a.hkv + h) * a.d : nullptr;
+      if (slot >= 0) page = static_cast<T*>(a.k_pages) + (slot * a.hkv + h) * a.d;
+    } else {
+      const int h = head - hq - a.hkv;
+      if (slot < 0) continue;
+      src = static_cast<const T*>(a.v) + tok * a.ldv + h * a.d;
+      dst = nullptr;
+      page = static_cast<T*>(a.v_pages) + (slot * a.hkv + h) * a.d;
+    }
+    alignas(16) T x1[V], x2[V];
+    *reinterpret_cast<uint4*>(x1) = *reinterpret_cast<const uint4*>(src + m);
+    *reinterpret_cast<uint4*>(x2) = *reinterpret_cast<const uint4*>(src + m + half);
+    if (rope && head < hq + a.hkv) {
+      const float2* c = cs + t * half + m;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float y1 = to_f32(x1[j]), y2 = to_f32(x2[j]);
+        x1[j] = from_f32<T>(y1 * c[j].x - y2 * c[j].y);
+        x2[j] = from_f32<T>(y2 * c[j].x + y1 * c[j].y);
+      }
+    }
+    if (dst) {
+      *reinterpret_cast<uint4*>(dst + m) = *reinterpret_cast<uint4*>(x1);
+      *reinterpret_cast<uint4*>(dst + m + half) = *reinterpret_cast<uint4*>(x2);
+    }
+    if (page) {
+      *reinterpret_cast<uint4*>(page + m) = *reinterpret_cast<uint4*>(x1);
+      *reinterpret_cast<uint4*>(page + m + half) = *reinterpret_cast<uint4*>(x2);
+    }
+  }
+}
+
+}  // namespace
+
+int launch_paged_schedule(const ScheduleArgs& a, cudaStream_t s) {
+  const size_t smem = sizeof(int32_t) * 2 * (static_cast<size_t>(a.B) + 1);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(paged_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  const int64_t want = (a.n_tokens + 4095) / 4096;   // 4 tokens per thread before another block starts
+  const int grid = static_cast<int>(want < 1 ? 1 : want > kSms ? kSms : want);
+  paged_schedule_kernel<<<grid, 1024, smem, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int launch_paged_append(const AppendArgs& a, cudaStream_t s) {
+  constexpr double kTwoPi = 6.283185307179586476925;
+  RopeFreqs f;
+  for (int m = 0; m < kMaxHalfDim; ++m)
+    f.omega[m] = (m < a.d / 2 && a.rope_theta > 0) ? pow(a.rope_theta, -2.0 * m / a.d) / kTwoPi : 0.0;
+  const int tpb = a.N >= 8 * kSms ? 4 : 1;
+  const int64_t grid = (a.N + tpb - 1) / tpb;
+  const size_t smem = sizeof(float2) * tpb * (a.d / 2);
+  if (a.dtype == PA_F32)
+    paged_append_kernel<float><<<static_cast<unsigned>(grid), 256, smem, s>>>(a, f, tpb);
+  else
+    paged_append_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), 256, smem, s>>>(a, f, tpb);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace pa

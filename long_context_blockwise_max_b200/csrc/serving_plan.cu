@@ -1,0 +1,335 @@
+// Work plan of an attention call over requests of different lengths, and
+// the merge of rows whose keys were cut into pieces.
+//
+// The lengths are on the device, so the plan is made there, by one block,
+// in the call itself: a list of pieces for the tile kernels (one per group
+// of rows, the deepest first, so that the short ones fill the end of the
+// launch), or, when there are too few to fill the SMs, the same rows with
+// their keys cut into about equal pieces; and the ranges of the decode
+// kernel's blocks.  The kernels behind it are launched for the most pieces
+// the arguments allow, and blocks without one return at once.
+#include <type_traits>
+
+#include "serving.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 1024;
+// A piece's fixed cost (prologue, first copies in flight, epilogue) in key
+// tiles, and the most (rows, kv head) pairs for which cutting keys is
+// looked at: from three waves of blocks on there is nothing to gain.
+constexpr int kPieceCost = 7;
+constexpr int kCutBelow = 3 * kSms;
+constexpr int kMaxCut = 64;
+
+struct Lens {
+  int64_t row0, q, kv;
+  int rows;      // packed (token, head) rows per kv head
+  bool small;    // decode kernel
+};
+
+__device__ __forceinline__ Lens lens_of(const AttendArgs& a, int b, int64_t max_kv, bool record) {
+  Lens r;
+  const int64_t lo = a.cu_q[b], hi = a.cu_q[b + 1];
+  r.row0 = lo;
+  r.q = hi - lo;
+  r.kv = a.kv_len ? a.kv_len[b] : r.q;
+  const bool bad = lo < 0 || hi < lo || hi > a.N || r.kv < 0 || r.kv > max_kv || (a.kv_len && r.q > a.max_q);
+  if (bad) {
+    if (record) set_status(a.status, PA_ERR_INVALID, b);
+    r.q = 0;
+    r.kv = 0;
+  }
+  const int64_t rows = r.q * (a.hq / a.hkv);
+  r.rows = static_cast<int>(rows < INT32_MAX ? rows : INT32_MAX);
+  r.small = r.rows <= a.small_rows;
+  return r;
+}
+
+__device__ __forceinline__ int depth_of(const Lens& r, int tok0, int tokens) {
+  const int64_t end = min(r.q, static_cast<int64_t>(tok0) + tokens);
+  return static_cast<int>((keys_seen(r.kv, r.q, end) + kPlanTile - 1) / kPlanTile);
+}
+
+__device__ __forceinline__ void put_piece(const AttendArgs& a, int at, int b, const Lens& r, int tok0, int kt0,
+                                          int kt1, int part) {
+  int4* dst = reinterpret_cast<int4*>(a.pieces + at);
+  dst[0] = make_int4(b, tok0, kt0, kt1);
+  dst[1] = make_int4(part, static_cast<int>(r.row0), static_cast<int>(r.q), static_cast<int>(r.kv));
+}
+
+__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(AttendArgs a, int64_t max_kv) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  int64_t* units = reinterpret_cast<int64_t*>(raw);          // [B + 1] decode key groups before request b
+  int32_t* items = reinterpret_cast<int32_t*>(units + a.B + 1);   // [B + 1] row groups before request b
+  __shared__ int64_t tmp[33];
+  __shared__ int hist[kBuckets];
+  __shared__ int deepest, n_merge;
+  __shared__ unsigned long long best;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < static_cast<int>(kStatusBytes / 4)) reinterpret_cast<int32_t*>(a.status)[tid] = 0;
+  for (int c = tid; c < a.decode_ctas; c += kPlanThreads) a.done[c] = 0;
+  if (tid == 0) {
+    units[0] = 0;
+    items[0] = 0;
+    deepest = 0;
+    n_merge = 0;
+    best = ~0ull;
+  }
+  for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
+  __syncthreads();
+  int64_t item_base = 0, unit_base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int64_t ni = 0, nu = 0;
+    if (b < a.B) {
+      const Lens r = lens_of(a, b, max_kv, true);
+      if (r.q > 0) {
+        if (r.small) {
+          const int64_t groups = (r.kv + kPlanTile - 1) / kPlanTile;
+          nu = (groups > 0 ? groups : 1) * a.hkv;
+        } else {
+          ni = (r.q + a.tile_tokens - 1) / a.tile_tokens;
+          atomicMax(&deepest, static_cast<int>((keys_seen(r.kv, r.q, r.q) + kPlanTile - 1) / kPlanTile));
+        }
+      }
+    }
+    int64_t all;
+    const int64_t xi = item_base + block_incl_scan<int64_t>(ni, tmp, &all);
+    item_base += all;
+    const int64_t xu = unit_base + block_incl_scan<int64_t>(nu, tmp, &all);
+    unit_base += all;
+    if (b < a.B) {
+      items[b + 1] = static_cast<int32_t>(xi < INT32_MAX ? xi : INT32_MAX);
+      units[b + 1] = xu;
+    }
+  }
+  __syncthreads();
+  // ---- decode: equal ranges of key groups, one per block ----------------
+  if (a.decode_ctas > 0) {
+    const int64_t each = unit_base / a.decode_ctas, more = unit_base % a.decode_ctas;
+    for (int c = tid; c < a.decode_ctas; c += kPlanThreads) {
+      const int64_t u0 = c * each + (c < more ? c : more);
+      DecodeStart st = {0, 0, 0, 0};
+      if (u0 < unit_base) {
+        st.b = upper_index(units, a.B + 1, u0);
+        const int groups = static_cast<int>((units[st.b + 1] - units[st.b]) / a.hkv);
+        const int64_t rem = u0 - units[st.b];
+        st.kvh = static_cast<int>(rem / groups);
+        st.unit = static_cast<int>(rem % groups);
+      }
+      *reinterpret_cast<int4*>(a.starts + c) = make_int4(st.b, st.kvh, st.unit, 0);
+    }
+  }
+  // ---- tiles --------------------------------------------------------------
+  const int64_t most = a.piece_cap;
+  const int n = static_cast<int>(item_base < most ? item_base : most);
+  if (item_base > most && tid == 0) set_status(a.status, PA_ERR_INVALID, a.B);   // rows counted twice
+  bool cut = a.part_cap > 0 && n > 0 && static_cast<int64_t>(n) * a.hkv < kCutBelow && n <= kPlanThreads &&
+             n <= a.item_cap && deepest > 1;
+  int parts = 1, chunk = deepest;
+  if (cut) {
+    // the number of cuts of the deepest rows that ends first: blocks run in
+    // waves of one per SM, or, past one wave, fill the SMs evenly with half
+    // a piece of slack; a cut adds the merge of its partial results
+    for (int s = warp + 1; s <= kMaxCut; s += kPlanThreads / 32) {
+      const int c = (deepest + s - 1) / s;
+      int np = 0;
+      float load = 0.f;
+      for (int i = lane; i < n; i += 32) {
+        const int b = upper_index(items, a.B + 1, i);
+        const Lens r = lens_of(a, b, max_kv, false);
+        const int d = depth_of(r, (i - items[b]) * a.tile_tokens, a.tile_tokens);
+        const int p = d > c ? (d + c - 1) / c : 1;
+        np += p;
+        load += static_cast<float>(d) + kPieceCost * p;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        np += __shfl_xor_sync(0xffffffffu, np, o);
+        load += __shfl_xor_sync(0xffffffffu, load, o);
+      }
+      if (lane == 0 && np <= a.part_cap) {
+        float cost = static_cast<float>(kPieceCost + c);
+        if (static_cast<int64_t>(np) * a.hkv > kSms)
+          cost = fmaxf(cost, load * a.hkv / kSms + 0.5f * (kPieceCost + c));
+        if (s > 1) cost += 3.f + s / 8.f;
+        atomicMin(&best, (static_cast<unsigned long long>(__float_as_uint(cost)) << 32) | s);
+      }
+    }
+    __syncthreads();
+    if (best != ~0ull) parts = static_cast<int>(best & 0xffffffffu);
+    chunk = (deepest + parts - 1) / parts;
+    cut = parts > 1;
+  }
+  int n_pieces = n;
+  if (cut) {
+    int b = 0, tok0 = 0, d = 0, p = 0;
+    Lens r = {};
+    if (tid < n) {
+      b = upper_index(items, a.B + 1, tid);
+      r = lens_of(a, b, max_kv, false);
+      tok0 = (tid - items[b]) * a.tile_tokens;
+      d = depth_of(r, tok0, a.tile_tokens);
+      p = d > chunk ? (d + chunk - 1) / chunk : 1;
+    }
+    int64_t all;
+    const int at = static_cast<int>(block_incl_scan<int64_t>(p, tmp, &all)) - p;
+    n_pieces = static_cast<int>(all);
+    for (int i = 0; i < p; ++i)
+      put_piece(a, at + i, b, r, tok0, static_cast<int>(static_cast<int64_t>(d) * i / p),
+                static_cast<int>(static_cast<int64_t>(d) * (i + 1) / p), p > 1 ? at + i : -1);
+    if (p > 1) {
+      const int k = atomicAdd(&n_merge, 1);
+      a.items[k] = {static_cast<int32_t>(r.row0) + tok0,
+                    static_cast<int32_t>(min(static_cast<int64_t>(a.tile_tokens), r.q - tok0)), at, p};
+    }
+  } else {
+    // deepest first: a counting sort by depth (the order inside a bucket is
+    // free; it changes no result)
+    auto bucket = [&](int d) {
+      return deepest > 0 ? kBuckets - 1 - static_cast<int>(static_cast<int64_t>(d) * (kBuckets - 1) / deepest) : 0;
+    };
+    for (int i = tid; i < n; i += kPlanThreads) {
+      const int b = upper_index(items, a.B + 1, i);
+      atomicAdd(&hist[bucket(depth_of(lens_of(a, b, max_kv, false), (i - items[b]) * a.tile_tokens,
+                                      a.tile_tokens))], 1);
+    }
+    __syncthreads();
+    const int h = hist[tid];
+    int64_t all;
+    const int before = static_cast<int>(block_incl_scan<int64_t>(h, tmp, &all)) - h;
+    hist[tid] = before;
+    __syncthreads();
+    for (int i = tid; i < n; i += kPlanThreads) {
+      const int b = upper_index(items, a.B + 1, i);
+      const Lens r = lens_of(a, b, max_kv, false);
+      const int tok0 = (i - items[b]) * a.tile_tokens;
+      const int d = depth_of(r, tok0, a.tile_tokens);
+      put_piece(a, atomicAdd(&hist[bucket(d)], 1), b, r, tok0, 0, d, -1);
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    a.head->n_pieces = n_pieces;
+    a.head->n_items = n_merge;
+    a.head->abort = 0;
+    a.head->decode_units = unit_base;
+  }
+}
+
+// Rows cut into pieces: lse = ln sum_p exp(lse_p), o = sum_p exp(lse_p - lse) o_p,
+// in piece order.  One warp per row.
+template <typename OT, int D>
+__global__ void __launch_bounds__(256) attend_merge_kernel(AttendArgs a) {
+  constexpr int VPL = D / 32;
+  if (static_cast<int>(blockIdx.x) >= a.head->n_items) return;
+  const MergeItem it = a.items[blockIdx.x];
+  const int kvh = blockIdx.y, g = a.hq / a.hkv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = it.n_tok * g;
+  const int64_t step = static_cast<int64_t>(a.hkv) * a.tile_rows;   // rows from one partial result to the next
+  const int64_t base = (static_cast<int64_t>(it.part0) * a.hkv + kvh) * a.tile_rows;
+  for (int r = blockIdx.z * 8 + warp; r < rows; r += gridDim.z * 8) {
+    const float* ls = a.part_lse + base + r;
+    float m = -INFINITY;
+    for (int p = lane; p < it.n_parts; p += 32) m = fmaxf(m, ls[p * step]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float sub = m == -INFINITY ? 0.f : m;   // a NaN stays one
+    float z = 0.f;
+    for (int p = lane; p < it.n_parts; p += 32) z += expf(ls[p * step] - sub);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    float acc[VPL] = {};
+    const float* src = a.part_o + (base + r) * D + lane * VPL;
+    if (z != 0.f) {
+      const float inv = 1.f / z;
+#pragma unroll 4
+      for (int p = 0; p < it.n_parts; ++p) {
+        const float w = expf(ls[p * step] - sub) * inv;
+        if (w == 0.f) continue;   // a piece without a visible key
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) acc[e] += w * src[p * step * D + e];
+      }
+    }
+    const int64_t row = static_cast<int64_t>(it.row0) + r / g;
+    const int head = kvh * g + r % g;
+    OT* dst = static_cast<OT*>(a.o) + (row * a.hq + head) * D + lane * VPL;
+#pragma unroll
+    for (int e = 0; e < VPL; ++e) dst[e] = from_f32<OT>(acc[e]);
+    if (lane == 0 && a.lse) a.lse[row * a.hq + head] = z == 0.f ? -INFINITY : sub + logf(z);
+  }
+}
+
+template <typename OT>
+void merge(const AttendArgs& a, cudaStream_t s) {
+  const dim3 grid(a.item_cap, a.hkv, (a.tile_rows + 31) / 32);
+  if (a.d == 128) attend_merge_kernel<OT, 128><<<grid, 256, 0, s>>>(a);
+  else attend_merge_kernel<OT, 64><<<grid, 256, 0, s>>>(a);
+}
+
+}  // namespace
+
+size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws) {
+  const int g = a.hq / a.hkv;
+  // fp32 rows per block: 16 when no request has more, 64 otherwise
+  a.tile_rows = a.max_q > 0 && static_cast<int64_t>(a.max_q) * g <= 16 ? 16 : 64;
+  a.tile_tokens = a.tile_rows / g;
+  a.small_rows = 0;
+  a.decode_ctas = 0;
+  const int64_t full = a.N / a.tile_tokens;
+  const int64_t groups = full + (a.B < a.N ? a.B : a.N);   // sum over requests of ceil(q / tile_tokens)
+  const int64_t deep = (max_kv + kPlanTile - 1) / kPlanTile;
+  a.part_cap = 0;
+  a.item_cap = 0;
+  if (full * a.hkv < kCutBelow && 2 * kSms / a.hkv >= 2 && deep > 1) {
+    const int64_t most = groups * deep;
+    a.part_cap = static_cast<int>(most < 2 * kSms / a.hkv ? most : 2 * kSms / a.hkv);
+    a.item_cap = static_cast<int>(groups < a.part_cap ? groups : a.part_cap);
+  }
+  a.piece_cap = static_cast<int>(groups > a.part_cap ? groups : a.part_cap);
+  char* w = static_cast<char*>(ws);
+  size_t off = 0;
+  auto take = [&](auto*& p, size_t count) {
+    using T = std::remove_reference_t<decltype(*p)>;
+    if (w != nullptr) p = reinterpret_cast<T*>(w + off);
+    off += align_up(sizeof(T) * count);
+  };
+  take(a.status, 1);
+  take(a.head, 1);
+  take(a.pieces, a.piece_cap);
+  take(a.items, a.item_cap);
+  take(a.starts, a.decode_ctas);
+  take(a.done, a.decode_ctas);
+  const size_t parts = static_cast<size_t>(a.part_cap) * a.hkv * a.tile_rows;
+  take(a.part_lse, parts);
+  take(a.part_o, parts * a.d);
+  take(a.dec_lse, static_cast<size_t>(a.decode_ctas) * 2 * 16);
+  take(a.dec_o, static_cast<size_t>(a.decode_ctas) * 2 * 16 * a.d);
+  return off;
+}
+
+int launch_attend(const AttendArgs& a, cudaStream_t s) {
+  const int64_t max_kv = a.block_table ? static_cast<int64_t>(a.max_pages) * a.page_size : a.N;
+  const size_t smem = (sizeof(int64_t) + sizeof(int32_t)) * (static_cast<size_t>(a.B) + 1);
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(attend_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  attend_plan_kernel<<<1, kPlanThreads, smem, s>>>(a, max_kv);
+  profile_begin(s);
+  const int rc = launch_attend_simt(a, s);
+  profile_end(s);
+  if (rc != PA_OK) return rc;
+  if (a.part_cap > 0) {
+    if (a.dtype == PA_F32) merge<float>(a, s);
+    else merge<__nv_bfloat16>(a, s);
+  }
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace pa

@@ -1,0 +1,212 @@
+// Attention of packed rows or of rows over pages on the fp32 units: the path
+// of fp32 inputs (every product and sum in fp32).
+//
+// Block = one piece: up to ROWS (token, query head) rows of one kv head
+// against its key tiles, 64 keys at a time through shared memory, 256
+// threads as 16 x 16: a thread has ROWS / 16 rows x 4 keys of the scores and
+// the same rows x D / 16 columns of o.  Online softmax in log2 units, the
+// running maximum and sum of a row kept by the 16 threads that share it.
+#include "serving.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kKeys = 64;
+
+template <int D, int ROWS>
+struct SimtCfg {
+  static constexpr int LDK = D + 4;              // 16 keys of a load fall on different banks
+  static constexpr int LDP = kKeys + 4;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + ROWS * D;
+  static constexpr int OFF_V = OFF_K + kKeys * LDK;
+  static constexpr int OFF_P = OFF_V + kKeys * D;
+  static constexpr int FLOATS = OFF_P + ROWS * LDP;
+  static constexpr int SMEM = FLOATS * 4 + kKeys * 8;
+};
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
+  using C = SimtCfg<D, ROWS>;
+  constexpr int R = ROWS / 16, CV = D / 64;      // rows, float4 columns of a thread
+  extern __shared__ __align__(16) float sm[];
+  float* sq = sm + C::OFF_Q;
+  float* sk = sm + C::OFF_K;
+  float* sv = sm + C::OFF_V;
+  float* sp = sm + C::OFF_P;
+  int64_t* slot = reinterpret_cast<int64_t*>(sm + C::FLOATS);
+  if (static_cast<int>(blockIdx.x) >= a.head->n_pieces) return;
+  const Piece pc = a.pieces[blockIdx.x];
+  const int kvh = blockIdx.y, g = a.hq / a.hkv;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int n_rows = min(a.tile_tokens, pc.q_len - pc.tok0) * g;
+  const float scale = static_cast<float>(kLog2e / sqrt(static_cast<double>(D)));
+  const T* Q = static_cast<const T*>(a.q);
+  const T* K = static_cast<const T*>(a.k);
+  const T* V = static_cast<const T*>(a.v);
+  for (int e = tid; e < ROWS * D; e += 256) {
+    const int r = e / D, m = e % D;
+    float x = 0.f;
+    if (r < n_rows) {
+      const int64_t row = static_cast<int64_t>(pc.row0) + pc.tok0 + r / g;
+      x = to_f32(Q[row * a.ldq + (kvh * g + r % g) * D + m]);
+    }
+    sq[e] = x;
+  }
+  int64_t lim[R];                                // last visible key of each row
+  float m_run[R], l_run[R], acc[R][4 * CV];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int r = ty * R + i;
+    lim[i] = r < n_rows ? static_cast<int64_t>(pc.kv_len) - pc.q_len + pc.tok0 + r / g : -1;
+    m_run[i] = -INFINITY;
+    l_run[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4 * CV; ++j) acc[i][j] = 0.f;
+  }
+  const int64_t lim_first = static_cast<int64_t>(pc.kv_len) - pc.q_len + pc.tok0;
+  const int64_t k1 = min(static_cast<int64_t>(pc.kt1) * kPlanTile,
+                         keys_seen(pc.kv_len, pc.q_len, min(pc.q_len, pc.tok0 + a.tile_tokens)));
+  for (int64_t c0 = static_cast<int64_t>(pc.kt0) * kPlanTile; c0 < k1; c0 += kKeys) {
+    __syncthreads();
+    if (tid < kKeys) {
+      const int64_t key = c0 + tid;
+      int64_t at = -1;
+      if (key < k1) at = a.block_table ? key_slot(a, pc.b, key) : pc.row0 + key;
+      slot[tid] = at;
+    }
+    __syncthreads();
+    for (int e = tid; e < kKeys * (D / 4); e += 256) {
+      const int key = e / (D / 4), m = (e % (D / 4)) * 4;
+      const int64_t at = slot[key];
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (at >= 0) {
+        const T* ks = K + at * a.ldk + kvh * D + m;
+        const T* vs = V + at * a.ldv + kvh * D + m;
+        x = make_float4(to_f32(ks[0]), to_f32(ks[1]), to_f32(ks[2]), to_f32(ks[3]));
+        y = make_float4(to_f32(vs[0]), to_f32(vs[1]), to_f32(vs[2]), to_f32(vs[3]));
+      }
+      *reinterpret_cast<float4*>(sk + key * C::LDK + m) = x;
+      *reinterpret_cast<float4*>(sv + key * D + m) = y;
+    }
+    __syncthreads();
+    // scores of rows ty * R + i and keys tx + 16 * j
+    float s[R][4];
+#pragma unroll
+    for (int i = 0; i < R; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll 4
+    for (int m = 0; m < D; m += 4) {
+      float4 q4[R], k4[4];
+#pragma unroll
+      for (int i = 0; i < R; ++i) q4[i] = *reinterpret_cast<const float4*>(sq + (ty * R + i) * D + m);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k4[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * C::LDK + m);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(q4[i].x, k4[j].x, s[i][j]);
+          s[i][j] = fmaf(q4[i].y, k4[j].y, s[i][j]);
+          s[i][j] = fmaf(q4[i].z, k4[j].z, s[i][j]);
+          s[i][j] = fmaf(q4[i].w, k4[j].w, s[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float mt = m_run[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = c0 + tx + 16 * j <= lim[i] ? s[i][j] * scale : -INFINITY;
+        mt = fmaxf(mt, s[i][j]);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+      const float sub = mt == -INFINITY ? 0.f : mt;   // a row without a visible key so far
+      const float alpha = fast_exp2(m_run[i] - sub);
+      m_run[i] = mt;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = fast_exp2(s[i][j] - sub);
+        sum += p;
+        sp[(ty * R + i) * C::LDP + tx + 16 * j] = p;
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l_run[i] = l_run[i] * alpha + sum;
+#pragma unroll
+      for (int j = 0; j < 4 * CV; ++j) acc[i][j] *= alpha;
+    }
+    __syncwarp();   // a row's 16 threads are in one warp
+    // a tile that some row does not see in full: there a masked key must add
+    // nothing even if its V is not finite, so its product is skipped
+    const bool whole = c0 + kKeys - 1 <= lim_first;
+#pragma unroll 4
+    for (int key = 0; key < kKeys; ++key) {
+      float p[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) p[i] = sp[(ty * R + i) * C::LDP + key];
+#pragma unroll
+      for (int j = 0; j < CV; ++j) {
+        const float4 v4 = *reinterpret_cast<const float4*>(sv + key * D + 64 * j + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (whole || c0 + key <= lim[i]) {
+            acc[i][4 * j] = fmaf(p[i], v4.x, acc[i][4 * j]);
+            acc[i][4 * j + 1] = fmaf(p[i], v4.y, acc[i][4 * j + 1]);
+            acc[i][4 * j + 2] = fmaf(p[i], v4.z, acc[i][4 * j + 2]);
+            acc[i][4 * j + 3] = fmaf(p[i], v4.w, acc[i][4 * j + 3]);
+          }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int r = ty * R + i;
+    if (r >= n_rows) continue;
+    const bool empty = l_run[i] == 0.f;   // no visible key
+    const float inv = empty ? 0.f : 1.f / l_run[i];
+    const float lse = empty ? -INFINITY : (m_run[i] + log2f(l_run[i])) * kLn2f;
+    if (pc.part >= 0) {
+      const int64_t at = (static_cast<int64_t>(pc.part) * a.hkv + kvh) * a.tile_rows + r;
+#pragma unroll
+      for (int j = 0; j < CV; ++j)
+        *reinterpret_cast<float4*>(a.part_o + at * D + 64 * j + 4 * tx) =
+            make_float4(acc[i][4 * j] * inv, acc[i][4 * j + 1] * inv, acc[i][4 * j + 2] * inv, acc[i][4 * j + 3] * inv);
+      if (tx == 0) a.part_lse[at] = lse;
+    } else {
+      const int64_t at = (static_cast<int64_t>(pc.row0) + pc.tok0 + r / g) * a.hq + kvh * g + r % g;
+      T* dst = static_cast<T*>(a.o) + at * D;
+#pragma unroll
+      for (int j = 0; j < CV; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[64 * j + 4 * tx + e] = from_f32<T>(acc[i][4 * j + e] * inv);
+      if (tx == 0 && a.lse) a.lse[at] = lse;
+    }
+  }
+}
+
+template <typename T, int D, int ROWS>
+int launch(const AttendArgs& a, cudaStream_t s) {
+  constexpr int smem = SimtCfg<D, ROWS>::SMEM;
+  if (cudaFuncSetAttribute(attend_simt_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return PA_ERR_CUDA;
+  attend_simt_kernel<T, D, ROWS><<<dim3(a.piece_cap, a.hkv), 256, smem, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <typename T>
+int launch_t(const AttendArgs& a, cudaStream_t s) {
+  if (a.tile_rows == 16) return a.d == 128 ? launch<T, 128, 16>(a, s) : launch<T, 64, 16>(a, s);
+  return a.d == 128 ? launch<T, 128, 64>(a, s) : launch<T, 64, 64>(a, s);
+}
+
+}  // namespace
+
+int launch_attend_simt(const AttendArgs& a, cudaStream_t s) {
+  return a.dtype == PA_F32 ? launch_t<float>(a, s) : launch_t<__nv_bfloat16>(a, s);
+}
+
+}  // namespace pa

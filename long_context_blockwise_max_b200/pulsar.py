@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libpulsar_b200.so")
 PA_F32, PA_BF16 = 0, 1
 PA_SCORE_MAX_IDF, PA_SCORE_MEAN_IDF, PA_SCORE_EVENLY_SPACED, PA_SCORE_ENTROPY, PA_SCORE_BM25 = 0, 1, 2, 3, 4
 _STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID", -2: "PA_ERR_UNSUPPORTED", -3: "PA_ERR_WORKSPACE",
-           -4: "PA_ERR_CUDA", -5: "PA_ERR_TIMEOUT", -6: "PA_ERR_RANGE"}
+           -4: "PA_ERR_CUDA", -5: "PA_ERR_TIMEOUT", -6: "PA_ERR_RANGE", -7: "PA_ERR_CAPACITY"}
 
 # Every symbol declared in include/pulsar.h.
 ABI_SYMBOLS = (
