@@ -110,7 +110,8 @@ struct AttendArgs {
 size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws);
 int launch_attend(const AttendArgs& a, cudaStream_t s);
 
-int launch_attend_simt(const AttendArgs& a, cudaStream_t s);
+int launch_attend_simt(const AttendArgs& a, cudaStream_t s);   // fp32
+int launch_attend_tc(const AttendArgs& a, cudaStream_t s);     // bf16
 
 // keys of a request that the first `n` of its new tokens see
 __host__ __device__ inline int64_t keys_seen(int64_t kv_len, int64_t q_len, int64_t n) {

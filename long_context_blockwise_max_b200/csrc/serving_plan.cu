@@ -276,9 +276,14 @@ void merge(const AttendArgs& a, cudaStream_t s) {
 
 size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws) {
   const int g = a.hq / a.hkv;
-  // fp32 rows per block: 16 when no request has more, 64 otherwise
-  a.tile_rows = a.max_q > 0 && static_cast<int64_t>(a.max_q) * g <= 16 ? 16 : 64;
-  a.tile_tokens = a.tile_rows / g;
+  if (a.dtype == PA_BF16) {
+    a.tile_rows = 256;                // two tiles of 128 rows
+    a.tile_tokens = 2 * (128 / g);
+  } else {
+    // fp32 rows per block: 16 when no request has more, 64 otherwise
+    a.tile_rows = a.max_q > 0 && static_cast<int64_t>(a.max_q) * g <= 16 ? 16 : 64;
+    a.tile_tokens = a.tile_rows / g;
+  }
   a.small_rows = 0;
   a.decode_ctas = 0;
   const int64_t full = a.N / a.tile_tokens;
@@ -322,7 +327,7 @@ int launch_attend(const AttendArgs& a, cudaStream_t s) {
     return PA_ERR_CUDA;
   attend_plan_kernel<<<1, kPlanThreads, smem, s>>>(a, max_kv);
   profile_begin(s);
-  const int rc = launch_attend_simt(a, s);
+  const int rc = a.dtype == PA_BF16 ? launch_attend_tc(a, s) : launch_attend_simt(a, s);
   profile_end(s);
   if (rc != PA_OK) return rc;
   if (a.part_cap > 0) {

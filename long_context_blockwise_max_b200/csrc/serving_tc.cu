@@ -1,0 +1,629 @@
+// Causal attention of packed prompts, and of new tokens over a paged cache,
+// on the sm_100a tensor cores (tcgen05 + TMEM + TMA), bf16.
+//
+// A block takes one piece of the plan (serving_plan.cu) for one kv head: up
+// to two tiles of 128 packed rows (a tile holds 128 / g tokens x the g query
+// heads of the group, so every K / V tile serves all of them and a request's
+// ragged end wastes less than one tile) against 128-key tiles.  12 warps:
+//   warp 0      TMA producer: Q once, then K / V tiles through 2-stage
+//               rings.  Packed rows are one box per 64 columns; a paged tile
+//               is one box per page, issued by as many lanes.
+//   warp 1      MMA issuer (one thread): S = Q K^T (bf16 x bf16 -> fp32 in
+//               TMEM, exact products) and O += P V (P bf16 from TMEM).
+//   warps 2-3   guard of V tiles that hold masked keys (below); warp 2 also
+//               allocates TMEM (512 columns: S0 | O0 | S1 | O1).
+//   warps 4-11  two softmax warpgroups, one thread per row; online softmax
+//               in log2 units, O rescaled only when the running maximum
+//               grows by more than 2^8.
+// With two row tiles, the warpgroups take one each and share every K / V
+// tile: while one runs its softmax the tensor core works on the other.  With
+// one (a chunk of at most 128 rows), they take alternate key tiles of the same
+// rows, each with its own maximum, sum and O, joined at the end, so a short
+// query streams its keys at the same rate per block.
+//
+// Guard: P is zero at a masked key, but zero times an infinity or NaN in its
+// V is NaN.  In tiles with keys that some row does not see, rows past the
+// request's last key are zeroed in shared memory, and a non-finite V element
+// is replaced by zero with its key noted per column (first +inf, -inf, NaN);
+// the epilogue gives rows that do see it the value the sum would have.
+//
+// Every wait on an mbarrier is bounded; on expiry the block records
+// PA_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and returns.
+#include <cudaTypedefs.h>
+
+#include "serving.h"
+#include "sm100.cuh"
+
+namespace pa {
+using namespace sm100;
+
+namespace {
+
+constexpr int kKeyTile = 128;
+static_assert(kKeyTile == kPlanTile, "the plan counts this kernel's key tiles");
+
+template <int D>
+struct SvCfg {
+  static constexpr int NKB = D / 64;                 // 128-byte column blocks along d
+  static constexpr int KB_BYTES = 128 * 128;         // 128 rows x 128 B
+  static constexpr int TILE_BYTES = NKB * KB_BYTES;  // 128 rows x D x 2 B
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = 2 * TILE_BYTES;
+  static constexpr int OFF_V = OFF_K + 2 * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_V + 2 * TILE_BYTES;
+  static constexpr int SMEM_BYTES = OFF_BAR + 8192;
+  static constexpr float SCALE = static_cast<float>(kLog2e / (D == 128 ? 11.31370849898476039 : 8.0));  // log2(e) / sqrt(d)
+  static constexpr uint32_t IDESC_QK = idesc_f16(128, 128, 1, 1, 0, 0);  // bf16 Q . bf16 K
+  static constexpr uint32_t IDESC_PV = idesc_f16(128, D, 1, 1, 0, 1);    // bf16 P . bf16 V (MN-major)
+};
+
+struct SvBars {
+  uint64_t q_full;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t vg_full[2];    // a guarded V tile has landed
+  uint64_t v_ready[2];    // ... and has been checked
+  uint64_t s_full[2], p_full[2], o_final[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int nonfinite;          // some guarded V element was not finite
+  int first[3][128];      // per column: first key with +inf, -inf, NaN
+  float ml[2][2][128];    // one row tile: both warpgroups' maximum and sum per row
+};
+static_assert(sizeof(SvBars) + 1024 <= 8192, "barriers and alignment slack");
+
+struct SvParams {
+  AttendArgs a;
+  int box_rows;     // keys per TMA box (a page, or a whole tile)
+  int oob_row;      // a row coordinate past the end of K and V: reads zeros
+};
+
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+template <int ID, int N>
+__device__ __forceinline__ void bar_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
+}
+template <int ID, int N>
+__device__ __forceinline__ void bar_arrive() {
+  asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(N) : "memory");
+}
+__device__ __forceinline__ bool bf16_nonfinite(uint32_t two) {
+  return (two & 0x7f80u) == 0x7f80u || (two & 0x7f800000u) == 0x7f800000u;
+}
+
+// One guarded V tile in shared memory (column blocks of 128 rows x 128 B,
+// 128-byte swizzle): rows from `first_row` on may be masked, rows from
+// `n_keys` on hold no key.  Run by 64 threads.
+template <int D>
+__device__ void guard_tile(uint8_t* v, int first_row, int n_keys, int key0, SvBars* bars, int tid) {
+  using C = SvCfg<D>;
+  constexpr int CH = D / 8;   // 16-byte chunks of a row
+  for (int i = first_row * CH + tid; i < 128 * CH; i += 64) {
+    const int r = i / CH, c = i % CH;
+    uint4* p = reinterpret_cast<uint4*>(v + (c >> 3) * C::KB_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    if (r >= n_keys) {
+      *p = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    uint4 x = *p;
+    if (bf16_nonfinite(x.x) || bf16_nonfinite(x.y) || bf16_nonfinite(x.z) || bf16_nonfinite(x.w)) {
+      uint16_t* e = reinterpret_cast<uint16_t*>(&x);
+      for (int k = 0; k < 8; ++k)
+        if ((e[k] & 0x7f80) == 0x7f80) {
+          const int kind = (e[k] & 0x7f) ? 2 : (e[k] >> 15);
+          atomicMin(&bars->first[kind][8 * c + k], key0 + r);
+          e[k] = 0;
+        }
+      *p = x;
+      bars->nonfinite = 1;
+    }
+  }
+}
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
+                                                           const __grid_constant__ CUtensorMap tmK,
+                                                           const __grid_constant__ CUtensorMap tmV,
+                                                           const __grid_constant__ SvParams p) {
+  using C = SvCfg<D>;
+  const AttendArgs& a = p.a;
+  if (static_cast<int>(blockIdx.x) >= a.head->n_pieces) return;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  SvBars* bars = reinterpret_cast<SvBars*>(smem + C::OFF_BAR);
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->vg_full[s], 1);
+      mbar_init(&bars->v_ready[s], 64);
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_full[s], 128);
+      mbar_init(&bars->o_final[s], 1);
+    }
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    bars->nonfinite = 0;
+    fence_mbar_init();
+  }
+  for (int i = threadIdx.x; i < 3 * 128; i += 384) bars->first[0][i] = INT32_MAX;
+  if (warp == 2) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  const Piece pc = a.pieces[blockIdx.x];
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int* abort = &bars->abort;
+  volatile int* gabort = &a.head->abort;
+  const int kvh = blockIdx.y, g = a.hq / a.hkv;
+  const int tpt = 128 / g;                           // tokens per row tile
+  const int ctx = pc.kv_len - pc.q_len;              // position of the first new token (may be negative)
+  const int n = pc.kt1 - pc.kt0;                     // key tiles of this piece
+  const bool two = pc.tok0 + tpt < pc.q_len;         // two row tiles
+  // key tiles of warpgroup t: with two row tiles those up to its last row's
+  // limit, of all; with one, every other
+  int nt[2];
+  if (two) {
+    const int seen = max(0, ctx + pc.tok0 + tpt);    // keys that tile 0 sees (it is full)
+    nt[0] = max(0, min(n, (seen + kKeyTile - 1) / kKeyTile - pc.kt0));
+    nt[1] = n;
+  } else {
+    nt[0] = (n + 1) / 2;
+    nt[1] = n / 2;
+  }
+  // tiles from jg on hold a key that the piece's first row does not see
+  const int jg = max(0, ctx + pc.tok0 + 1) / kKeyTile;
+  const int g0 = max(0, jg - pc.kt0);                // first guarded tile of this piece
+  auto fail = [&](int where) {
+    *abort = 1;
+    *gabort = 1;
+    set_status(a.status, PA_ERR_TIMEOUT, static_cast<int>(blockIdx.x), where);
+  };
+  auto wait_one = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort, a.wait_limit_ns, gabort); };
+  // the same for a whole warp, one answer for all lanes
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const int nbox = kKeyTile / p.box_rows;
+    // row coordinate of this lane's box of tile j
+    auto row_of = [&](int j) -> int {
+      if (!PAGED) return pc.row0 + j * kKeyTile;
+      const int64_t key = static_cast<int64_t>(j) * kKeyTile + lane * p.box_rows;
+      if (lane >= nbox || key >= pc.kv_len) return p.oob_row;
+      const int64_t slot = key_slot(a, pc.b, key);
+      return slot < 0 ? p.oob_row : static_cast<int>(slot);
+    };
+    int row = n > 0 ? row_of(pc.kt0) : 0;
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      const int qt = two ? 2 : 1;
+      const int q_bytes = tpt * g * 128 * C::NKB;
+      mbar_arrive_expect_tx(&bars->q_full, qt * q_bytes);
+      for (int t = 0; t < qt; ++t)
+        for (int kb = 0; kb < C::NKB; ++kb)
+          tma_load_3d(sQ + t * C::TILE_BYTES + kb * C::KB_BYTES, &tmQ, &bars->q_full, kb * 64, kvh * g,
+                      pc.row0 + pc.tok0 + t * tpt);
+    }
+    int n_k = 0, n_v = 0;   // K and V tiles issued
+    for (int jj = 0; jj < n; ++jj) {
+      const int st = jj & 1;
+      const uint32_t ph = (jj >> 1) & 1;
+      const int next = jj + 1 < n ? row_of(pc.kt0 + jj + 1) : 0;
+      if (!wait(&bars->k_empty[st], ph ^ 1)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], C::TILE_BYTES);
+      __syncwarp();
+      if (lane < nbox)
+        for (int kb = 0; kb < C::NKB; ++kb)
+          tma_load_3d(sK + st * C::TILE_BYTES + kb * C::KB_BYTES + lane * p.box_rows * 128, &tmK, &bars->k_full[st],
+                      kb * 64, kvh, row);
+      ++n_k;
+      if (!wait(&bars->v_empty[st], ph ^ 1)) break;
+      uint64_t* full = jj >= g0 ? &bars->vg_full[st] : &bars->v_full[st];
+      if (lane == 0) mbar_arrive_expect_tx(full, C::TILE_BYTES);
+      __syncwarp();
+      if (lane < nbox)
+        for (int kb = 0; kb < C::NKB; ++kb)
+          tma_load_3d(sV + st * C::TILE_BYTES + kb * C::KB_BYTES + lane * p.box_rows * 128, &tmV, full, kb * 64,
+                      kvh, row);
+      ++n_v;
+      row = next;
+    }
+    if (lane == 0) {
+      if (n_v < n) fail(1);
+      // Drain: every copy this warp started has landed before the block ends.
+      int zero = 0;
+      mbar_wait(&bars->q_full, 0, &zero, a.wait_limit_ns);
+      for (int s = 0; s < 2; ++s) {
+        const int uk = (n_k + 1 - s) >> 1;                             // K tiles of stage s
+        if (uk > 0) mbar_wait(&bars->k_full[s], (uk - 1) & 1, &zero, a.wait_limit_ns);
+        const int nu = min(n_v, g0);                                   // unguarded V tiles
+        const int uv = (nu + 1 - s) >> 1;
+        if (uv > 0) mbar_wait(&bars->v_full[s], (uv - 1) & 1, &zero, a.wait_limit_ns);
+        const int ng = n_v - nu;                                       // guarded ones, from tile g0 on
+        const int ug = (ng + 1 - ((s ^ g0) & 1)) >> 1;
+        if (ug > 0) mbar_wait(&bars->vg_full[s], (ug - 1) & 1, &zero, a.wait_limit_ns);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0) {
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(sV), C::KB_BYTES, 1024);
+      auto qk = [&](int t, int st) {
+        const uint32_t d_tmem = tmem + t * 256;
+        const uint64_t qd = sdesc_add(q_desc, two ? t * C::TILE_BYTES : 0);
+        const uint64_t kd = sdesc_add(k_desc, st * C::TILE_BYTES);
+#pragma unroll
+        for (int kb = 0; kb < C::NKB; ++kb)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_ss(d_tmem, sdesc_add(qd, kb * C::KB_BYTES + ks * 32), sdesc_add(kd, kb * C::KB_BYTES + ks * 32),
+                   C::IDESC_QK, (kb | ks) != 0);
+      };
+      auto pv = [&](int t, int st, int acc) {
+        const uint32_t d_tmem = tmem + t * 256 + 128;
+        const uint64_t vd = sdesc_add(v_desc, st * C::TILE_BYTES);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts(d_tmem, tmem + t * 256 + ks * 8, sdesc_add(vd, ks * 2048), C::IDESC_PV, (acc | ks) != 0);
+      };
+      auto wait_k = [&](int jj) { return wait_one(&bars->k_full[jj & 1], (jj >> 1) & 1); };
+      auto wait_v = [&](int jj) {
+        return jj < g0 ? wait_one(&bars->v_full[jj & 1], (jj >> 1) & 1) : wait_one(&bars->v_ready[jj & 1], ((jj - g0) >> 1) & 1);
+      };
+      bool ok = wait_one(&bars->q_full, 0);
+      if (!ok) fail(3);
+      if (two) {
+        for (int jj = 0; ok && jj < n; ++jj) {
+          const int st = jj & 1, st1 = st ^ 1;
+          if (jj == 0) {
+            if (!wait_k(0)) { fail(4); break; }
+            tc_fence_after();
+            for (int t = 0; t < 2; ++t)
+              if (nt[t] > 0) {
+                qk(t, 0);
+                mma_commit(&bars->s_full[t]);
+              }
+            mma_commit(&bars->k_empty[0]);
+          }
+          // V_j and K_{j+1} first, while the tensor pipe still runs the other
+          // tile's MMAs, so that nothing stands between P and its products
+          if (!wait_v(jj)) { fail(6); break; }
+          if (jj + 1 < n && !wait_k(jj + 1)) { fail(7); break; }
+          for (int t = 0; t < 2; ++t) {
+            if (jj < nt[t]) {
+              if (!wait_one(&bars->p_full[t], jj & 1)) { fail(5); ok = false; break; }
+              tc_fence_after();
+              pv(t, st, jj > 0);
+              if (jj == nt[t] - 1) mma_commit(&bars->o_final[t]);
+            }
+            if (t == 1) mma_commit(&bars->v_empty[st]);
+            if (jj + 1 < nt[t]) {
+              qk(t, st1);
+              mma_commit(&bars->s_full[t]);
+            }
+          }
+          if (ok && jj + 1 < n) mma_commit(&bars->k_empty[st1]);
+        }
+      } else if (ok && n > 0) {
+        for (int jj = 0; jj < min(n, 2); ++jj) {
+          if (!wait_k(jj)) { fail(4); ok = false; break; }
+          tc_fence_after();
+          qk(jj, jj);
+          mma_commit(&bars->s_full[jj]);
+          mma_commit(&bars->k_empty[jj]);
+        }
+        for (int jj = 0; ok && jj < n; ++jj) {
+          const int t = jj & 1, i = jj >> 1;
+          if (!wait_v(jj)) { fail(6); break; }
+          if (jj + 2 < n && !wait_k(jj + 2)) { fail(7); break; }
+          if (!wait_one(&bars->p_full[t], i & 1)) { fail(5); break; }
+          tc_fence_after();
+          pv(t, t, i > 0);
+          if (i == nt[t] - 1) mma_commit(&bars->o_final[t]);
+          mma_commit(&bars->v_empty[t]);
+          if (jj + 2 < n) {
+            qk(t, t);
+            mma_commit(&bars->s_full[t]);
+            mma_commit(&bars->k_empty[t]);
+          }
+        }
+      }
+      // Drain: all MMAs issued by this thread complete before TMEM is freed.
+      int zero = 0;
+      mma_commit(&bars->drain);
+      mbar_wait(&bars->drain, 0, &zero, a.wait_limit_ns);
+    }
+  } else if (warp < 4) {
+    // ---------------------------------------------------------- V guard
+    const int tid = threadIdx.x - 64;
+    const int lim_first = ctx + pc.tok0;
+    for (int jj = g0; jj < n; ++jj) {
+      const int st = jj & 1, i = (jj - g0) >> 1;
+      if (!wait(&bars->vg_full[st], i & 1)) { if (lane == 0) fail(11); break; }
+      const int key0 = (pc.kt0 + jj) * kKeyTile;
+      guard_tile<D>(sV + st * C::TILE_BYTES, max(0, lim_first + 1 - key0), pc.kv_len - key0, key0, bars, tid);
+      fence_async_smem();
+      mbar_arrive(&bars->v_ready[st]);
+    }
+    bar_arrive<1, 320>();
+  } else {
+    // -------------------------------------------------------------- softmax
+    const int t = warp >= 8 ? 1 : 0;
+    const int sub = warp & 3;
+    const int rl = sub * 32 + lane;
+    const int tok_t = pc.tok0 + (two ? t * tpt : 0);     // first token of this warpgroup's rows
+    const int tok = tok_t + rl / g;
+    const bool valid = rl < tpt * g && tok < pc.q_len;
+    const int lim = valid ? ctx + tok : pc.kv_len - 1;   // last visible key
+    const int lim_w = ctx + tok_t + sub * 32 / g;        // the smallest of this warp's rows
+    const uint32_t s_tmem = tmem + (static_cast<uint32_t>(sub * 32) << 16) + t * 256;
+    const uint32_t o_tmem = s_tmem + 128;
+    const int my = nt[t];
+    const uint64_t sc2 = f2_pack(C::SCALE, C::SCALE);
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = true;
+    for (int i = 0; i < my; ++i) {
+      const int key0 = (pc.kt0 + (two ? i : 2 * i + t)) * kKeyTile;
+      if (!wait(&bars->s_full[t], i & 1)) { fail(9); ok = false; break; }
+      tc_fence_after();
+      uint32_t sr[128];
+      tmem_ld_x128(s_tmem, sr);
+      if (key0 + kKeyTile - 1 > lim_w) {
+        const int rel = lim - key0;                      // columns <= rel are visible
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+          if (e > rel) sr[e] = __float_as_uint(-INFINITY);
+      }
+      float mx[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx[e] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 64; ++e)
+        mx[e & 7] = fmax3(mx[e & 7], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+      const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
+      const float m_new = fmaxf(m_run, mt);
+      const bool need = (m_new - m_run) * C::SCALE > 8.f;   // lazy rescale: only when P could exceed 2^8
+      float alpha = 1.f;
+      if (need) {
+        alpha = fast_exp2((m_run - m_new) * C::SCALE);
+        m_run = m_new;
+      }
+      const float m_use = (m_run == -INFINITY) ? 0.f : m_run * C::SCALE;
+      const uint64_t nm2 = f2_pack(-m_use, -m_use);
+      uint64_t acc2[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc2[e] = 0ull;   // two 0.0f
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float x0, x1, p0, p1;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])),
+                           sc2, nm2), x0, x1);
+          p0 = fast_exp2(x0);
+          p1 = fast_exp2(x1);
+          acc2[e & 3] = f2_add(acc2[e & 3], f2_pack(p0, p1));
+          pk[e] = pack2(p0, p1);
+        }
+        tmem_st_x16(s_tmem + 16 * c, pk);
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float a0, a1;
+        f2_unpack(acc2[e], a0, a1);
+        sum += a0 + a1;
+      }
+      l_run = l_run * alpha + sum;
+      if (i > 0 && __any_sync(0xffffffffu, need)) {
+        // O was last written by the previous PV, which completed before this
+        // S (the commit signalling S covers every earlier MMA).
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld_x32(o_tmem + 32 * c, ov);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+          tmem_st_x32(o_tmem + 32 * c, ov);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&bars->p_full[t]);
+    }
+    bar_sync<1, 320>();   // the guard's notes are complete
+    // Rows' final maximum and sum.  Weights w0, w1 of the two O's (one row
+    // tile) or w0 of its own (two).
+    const int n_other = nt[t ^ 1];
+    if (ok && (my > 0 || (!two && n_other > 0))) {
+      if (my > 0 && !wait(&bars->o_final[t], 0)) { fail(10); ok = false; }
+      if (ok && !two && n_other > 0 && !wait(&bars->o_final[t ^ 1], 0)) { fail(10); ok = false; }
+    } else if (ok) {
+      // no key tile: nothing was computed, but Q's copy may still be landing
+      // in the memory that stages the output
+      if (!wait(&bars->q_full, 0)) { fail(10); ok = false; }
+    }
+    float w_own = 1.f, w_oth = 0.f;
+    if (!two) {
+      bars->ml[t][0][rl] = m_run;
+      bars->ml[t][1][rl] = l_run;
+      bar_sync<2, 256>();
+      const float m2 = bars->ml[t ^ 1][0][rl], l2 = bars->ml[t ^ 1][1][rl];
+      const float m = fmaxf(m_run, m2);
+      if (m != -INFINITY) {
+        w_own = fast_exp2((m_run - m) * C::SCALE);
+        w_oth = fast_exp2((m2 - m) * C::SCALE);
+      }
+      l_run = l_run * w_own + l2 * w_oth;
+      m_run = m;
+    }
+    if (ok) {
+      tc_fence_after();
+      const bool empty = l_run == 0.f;               // no visible key (a NaN sum is not zero)
+      const float inv = empty ? 0.f : 1.f / l_run;
+      const float lse = empty ? -INFINITY : ((m_run == -INFINITY ? 0.f : m_run * C::SCALE) + log2f(l_run)) * kLn2f;
+      w_own *= inv;
+      w_oth *= inv;
+      const bool odd = *reinterpret_cast<volatile int*>(&bars->nonfinite) != 0;
+      // with one row tile each warpgroup writes half of the columns
+      constexpr int CHUNKS = D / 32;
+      const int c0 = two ? 0 : t * (CHUNKS / 2), nc = two ? CHUNKS : CHUNKS / 2;
+      const uint32_t o_oth = tmem + (static_cast<uint32_t>(sub * 32) << 16) + (t ^ 1) * 256 + 128;
+      // staging of this warp's rows for whole-row stores, in Q's memory
+      // (every QK^T has been read by now)
+      uint8_t* stage = sQ + (warp - 4) * 32 * D * 2;
+      const int64_t prow = (static_cast<int64_t>(pc.part) * a.hkv + kvh) * a.tile_rows + (two ? t * tpt * g : 0) + rl;
+      for (int ci = 0; ci < nc; ++ci) {
+        const int c = c0 + ci;
+        float v[32];
+        uint32_t ov[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        if (my > 0) {
+          tmem_ld_x32(o_tmem + 32 * c, ov);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = empty ? 0.f : __uint_as_float(ov[e]) * w_own;
+        }
+        if (!two && n_other > 0) {
+          tmem_ld_x32(o_oth + 32 * c, ov);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] += empty ? 0.f : __uint_as_float(ov[e]) * w_oth;
+        }
+        if (odd) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int col = 32 * c + e;
+            const bool pos = bars->first[0][col] <= lim, neg = bars->first[1][col] <= lim;
+            if (bars->first[2][col] <= lim || (pos && neg)) v[e] = __int_as_float(0x7fc00000);
+            else if (pos) v[e] += INFINITY;
+            else if (neg) v[e] -= INFINITY;
+          }
+        }
+        if (pc.part >= 0) {
+          if (valid) {
+            float4* d4 = reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d4[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int ch = 4 * c + e;     // 16-byte chunk of the row, spread over the banks by row
+            *reinterpret_cast<uint4*>(stage + lane * D * 2 + ((ch ^ (lane & 7)) << 4)) =
+                make_uint4(pack2(v[8 * e], v[8 * e + 1]), pack2(v[8 * e + 2], v[8 * e + 3]),
+                           pack2(v[8 * e + 4], v[8 * e + 5]), pack2(v[8 * e + 6], v[8 * e + 7]));
+          }
+        }
+      }
+      if (pc.part >= 0) {
+        if (valid && (two || t == 0)) a.part_lse[prow] = lse;
+      } else {
+        if (valid && (two || t == 0) && a.lse)
+          a.lse[(static_cast<int64_t>(pc.row0) + tok) * a.hq + kvh * g + rl % g] = lse;
+        __syncwarp();
+        const int per = 4 * nc;           // 16-byte chunks of a row here: a power of two
+        const int rows_per = 32 / per;    // rows per store of the warp
+        for (int r = lane / per; r < 32; r += rows_per) {
+          const int row = sub * 32 + r, rt = tok_t + row / g;
+          if (row >= tpt * g || rt >= pc.q_len) continue;
+          const int ch = 4 * c0 + lane % per;
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + r * D * 2 + ((ch ^ (r & 7)) << 4));
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) +
+                               ((static_cast<int64_t>(pc.row0) + rt) * a.hq + kvh * g + row % g) * D + 8 * ch;
+          *reinterpret_cast<uint4*>(dst) = x;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// 16-bit tensor [rows][heads][d] with a row stride of ld elements, boxes of
+// 64 columns x `box_heads` x `box_rows`, 128-byte swizzle.
+bool rows_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int64_t ld, int box_heads,
+              int box_rows) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool PAGED>
+int launch_tc(const AttendArgs& a, cudaStream_t s) {
+  using C = SvCfg<D>;
+  const int g = a.hq / a.hkv;
+  SvParams p;
+  p.a = a;
+  p.box_rows = PAGED && a.page_size < kKeyTile ? a.page_size : kKeyTile;
+  // an empty cache has no page to read: every box is out of range, and the
+  // map is made over q only to have an address
+  const int64_t rows = a.n_slots > 0 ? a.n_slots : 1;
+  p.oob_row = static_cast<int>(rows);
+  CUtensorMap mq, mk, mv;
+  const void* k = a.n_slots > 0 ? a.k : a.q;
+  const void* v = a.n_slots > 0 ? a.v : a.q;
+  if (!rows_map(&mq, a.q, a.N, a.hq, D, a.ldq, g, 128 / g) ||
+      !rows_map(&mk, k, rows, a.hkv, D, a.ldk, 1, p.box_rows) ||
+      !rows_map(&mv, v, rows, a.hkv, D, a.ldv, 1, p.box_rows))
+    return PA_ERR_CUDA;
+  if (cudaFuncSetAttribute(attend_tc_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
+      cudaSuccess)
+    return PA_ERR_CUDA;
+  attend_tc_kernel<D, PAGED><<<dim3(a.piece_cap, a.hkv), 384, C::SMEM_BYTES, s>>>(mq, mk, mv, p);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_attend_tc(const AttendArgs& a, cudaStream_t s) {
+  if (a.block_table)
+    return a.d == 128 ? launch_tc<128, true>(a, s) : launch_tc<64, true>(a, s);
+  return a.d == 128 ? launch_tc<128, false>(a, s) : launch_tc<64, false>(a, s);
+}
+
+}  // namespace pa
