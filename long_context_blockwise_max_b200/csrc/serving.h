@@ -11,6 +11,7 @@ constexpr int kMaxRequests = 8192;   // prefix sums of a step are staged in shar
 constexpr int kMaxGroup = 64;        // query heads per kv head: a tile holds at least one token
 constexpr int kSms = 148;
 constexpr int kPlanTile = 128;       // keys per unit of planned work
+constexpr int kDecodeRows = 16;      // most rows per kv head of the decode kernel (one MMA's)
 
 struct ScheduleArgs {
   const int32_t *q_len, *kv_len;
@@ -89,6 +90,7 @@ struct AttendArgs {
   int32_t tile_tokens;            // new tokens per piece
   int32_t tile_rows;              // rows a partial result has room for
   int32_t small_rows;             // requests of at most so many rows go to the decode kernel
+  int32_t tiles;                  // whether a tile kernel runs
   int32_t piece_cap;              // pieces the workspace has room for
   int32_t part_cap;               // partial results it has room for, per kv head; 0: never cut
   int32_t item_cap;
@@ -112,6 +114,7 @@ int launch_attend(const AttendArgs& a, cudaStream_t s);
 
 int launch_attend_simt(const AttendArgs& a, cudaStream_t s);   // fp32
 int launch_attend_tc(const AttendArgs& a, cudaStream_t s);     // bf16
+int launch_attend_decode(const AttendArgs& a, cudaStream_t s); // bf16, few rows
 
 // keys of a request that the first `n` of its new tokens see
 __host__ __device__ inline int64_t keys_seen(int64_t kv_len, int64_t q_len, int64_t n) {

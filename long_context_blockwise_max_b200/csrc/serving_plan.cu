@@ -284,14 +284,21 @@ size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws) {
     a.tile_rows = a.max_q > 0 && static_cast<int64_t>(a.max_q) * g <= 16 ? 16 : 64;
     a.tile_tokens = a.tile_rows / g;
   }
+  // Rows per kv head up to which a request is the decode kernel's.  A call
+  // whose requests are long on average leaves them all to the tile kernel:
+  // its few short ones cost less there than another launch.
   a.small_rows = 0;
-  a.decode_ctas = 0;
-  const int64_t full = a.N / a.tile_tokens;
-  const int64_t groups = full + (a.B < a.N ? a.B : a.N);   // sum over requests of ceil(q / tile_tokens)
+  if (a.dtype == PA_BF16 && a.max_q > 0 &&
+      (static_cast<int64_t>(a.max_q) * g <= kDecodeRows || a.N < static_cast<int64_t>(a.B) * a.max_q))
+    a.small_rows = kDecodeRows;
+  a.decode_ctas = a.small_rows > 0 ? kSms : 0;
+  a.tiles = a.small_rows == 0 || static_cast<int64_t>(a.max_q) * g > a.small_rows;
+  const int64_t full = a.tiles ? a.N / a.tile_tokens : 0;
+  const int64_t groups = a.tiles ? full + (a.B < a.N ? a.B : a.N) : 0;   // sum over requests of ceil(q / tile_tokens)
   const int64_t deep = (max_kv + kPlanTile - 1) / kPlanTile;
   a.part_cap = 0;
   a.item_cap = 0;
-  if (full * a.hkv < kCutBelow && 2 * kSms / a.hkv >= 2 && deep > 1) {
+  if (a.tiles && full * a.hkv < kCutBelow && 2 * kSms / a.hkv >= 2 && deep > 1) {
     const int64_t most = groups * deep;
     a.part_cap = static_cast<int>(most < 2 * kSms / a.hkv ? most : 2 * kSms / a.hkv);
     a.item_cap = static_cast<int>(groups < a.part_cap ? groups : a.part_cap);
@@ -327,7 +334,9 @@ int launch_attend(const AttendArgs& a, cudaStream_t s) {
     return PA_ERR_CUDA;
   attend_plan_kernel<<<1, kPlanThreads, smem, s>>>(a, max_kv);
   profile_begin(s);
-  const int rc = a.dtype == PA_BF16 ? launch_attend_tc(a, s) : launch_attend_simt(a, s);
+  int rc = PA_OK;
+  if (a.decode_ctas > 0) rc = launch_attend_decode(a, s);
+  if (rc == PA_OK && a.tiles) rc = a.dtype == PA_BF16 ? launch_attend_tc(a, s) : launch_attend_simt(a, s);
   profile_end(s);
   if (rc != PA_OK) return rc;
   if (a.part_cap > 0) {
