@@ -20,7 +20,7 @@ struct ScheduleArgs {
   int64_t table_stride;
   int32_t max_pages;
   const int32_t* free_pages;
-  int32_t n_free, page_size;
+  int32_t n_free, page_shift;
   int64_t n_tokens;
   int32_t *cu_q, *kv_len_out, *positions, *slots, *n_used;
   DeviceStatus* status;
@@ -68,7 +68,7 @@ struct PlanHead {
   int32_t n_pieces;     // pieces of the tile kernels, per kv head
   int32_t n_items;      // entries of the merge list
   int32_t abort;        // a bounded wait ran out somewhere
-  int32_t pad;
+  int32_t heads_inner;  // order of the tile kernels' blocks (piece_of_block)
   int64_t decode_units; // key groups of the decode kernel, over kv heads
 };
 
@@ -91,6 +91,7 @@ struct AttendArgs {
   int32_t tile_rows;              // rows a partial result has room for
   int32_t small_rows;             // requests of at most so many rows go to the decode kernel
   int32_t tiles;                  // whether a tile kernel runs
+  int32_t slots;                  // blocks of it that run at once
   int32_t piece_cap;              // pieces the workspace has room for
   int32_t part_cap;               // partial results it has room for, per kv head; 0: never cut
   int32_t item_cap;
@@ -113,6 +114,7 @@ size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws);
 int launch_attend(const AttendArgs& a, cudaStream_t s);
 
 int launch_attend_simt(const AttendArgs& a, cudaStream_t s);   // fp32
+int simt_blocks_per_sm(const AttendArgs& a);
 int launch_attend_tc(const AttendArgs& a, cudaStream_t s);     // bf16
 int launch_attend_decode(const AttendArgs& a, cudaStream_t s); // bf16, few rows
 
@@ -122,7 +124,57 @@ __host__ __device__ inline int64_t keys_seen(int64_t kv_len, int64_t q_len, int6
   return k < 0 ? 0 : k;
 }
 
+// Launch attribute of a kernel that may be set up while the one before it
+// in the stream still runs; it calls grid_dep_wait() before it reads anything
+// that kernel (or one before) wrote.
+inline cudaLaunchAttribute overlap_attr() {
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  return at;
+}
+template <typename... P, typename... A>
+int launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at = overlap_attr();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// Blocks of a tile kernel: the most pieces the arguments allow, times kv heads.
+inline unsigned tile_blocks(const AttendArgs& a) {
+  return static_cast<unsigned>(a.piece_cap) * static_cast<unsigned>(a.hkv);
+}
+
 #ifdef __CUDACC__
+// Piece and kv head of this block; false if there is none.  Blocks that run
+// together share one kv head's K and V (which then stay in L2 however long
+// the caches are), or, when all of K and V fit there anyway, take the deepest
+// pieces of every head first, so that the launch ends with short ones.
+__device__ __forceinline__ bool piece_of_block(const AttendArgs& a, int* at, int* kvh) {
+  const unsigned n = static_cast<unsigned>(a.head->n_pieces), i = blockIdx.x;
+  if (i >= n * static_cast<unsigned>(a.hkv)) return false;
+  if (a.head->heads_inner) {
+    *at = static_cast<int>(i / static_cast<unsigned>(a.hkv));
+    *kvh = static_cast<int>(i % static_cast<unsigned>(a.hkv));
+  } else {
+    *at = static_cast<int>(i % n);
+    *kvh = static_cast<int>(i / n);
+  }
+  return true;
+}
+
+// Waits until the kernels before this one in the stream have ended and their
+// writes are visible.
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel of the stream be set up.
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // Slot of key `key` of request b, or -1 (recorded) when its page is not in
 // the cache.
 __device__ __forceinline__ int64_t key_slot(const AttendArgs& a, int b, int64_t key) {
@@ -146,23 +198,29 @@ __device__ __forceinline__ T warp_incl_scan(T x) {
   return x;
 }
 
-// Inclusive scan over a block of 1024 threads; *total receives the sum.
-// `tmp` has 33 elements; every thread of the block calls it.
+// Inclusive scans of x and y over the block (a multiple of 32 threads, at most
+// 1024); *x_all and *y_all receive the sums.  Every warp scans the warps' sums
+// for itself, so that one barrier is enough.  `tmp` has 64 elements and must
+// not be in use by an earlier scan (alternate two).
 template <typename T>
-__device__ __forceinline__ T block_incl_scan(T x, T* tmp, T* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ void block_incl_scan2(T& x, T& y, T* tmp, T* x_all, T* y_all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   x = warp_incl_scan(x);
-  if (lane == 31) tmp[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    const T w = warp_incl_scan(tmp[lane]);
-    tmp[lane] = w;
+  y = warp_incl_scan(y);
+  if (lane == 31) {
+    tmp[warp] = x;
+    tmp[32 + warp] = y;
   }
   __syncthreads();
-  const T before = warp > 0 ? tmp[warp - 1] : T(0);
-  *total = tmp[31];
-  __syncthreads();
-  return before + x;
+  const T wx = warp_incl_scan(lane < warps ? tmp[lane] : T(0));
+  const T wy = warp_incl_scan(lane < warps ? tmp[32 + lane] : T(0));
+  const T bx = __shfl_sync(0xffffffffu, wx, warp > 0 ? warp - 1 : 0), by = __shfl_sync(0xffffffffu, wy, warp > 0 ? warp - 1 : 0);
+  *x_all = __shfl_sync(0xffffffffu, wx, 31);
+  *y_all = __shfl_sync(0xffffffffu, wy, 31);
+  if (warp > 0) {
+    x += bx;
+    y += by;
+  }
 }
 
 // Largest i in [0, n) with pre[i] <= x (pre[0] <= x; pre non-decreasing).

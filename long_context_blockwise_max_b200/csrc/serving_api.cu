@@ -48,13 +48,19 @@ int check_batch(int32_t B, int64_t N) {
   return PA_OK;
 }
 
+int32_t log2_of(int32_t power) {
+  int32_t s = 0;
+  while ((1 << s) < power) ++s;
+  return s;
+}
+
 AttendArgs attend_args(int dtype, int64_t N, int32_t B, int32_t max_q, int32_t max_pages, int32_t page_size,
                        int32_t hq, int32_t hkv, int32_t d) {
   AttendArgs a = {};
   a.dtype = dtype;
   a.N = N; a.B = B; a.max_q = max_q;
   a.max_pages = max_pages; a.page_size = page_size;
-  while ((1 << a.page_shift) < page_size) ++a.page_shift;
+  a.page_shift = log2_of(page_size);
   a.hq = hq; a.hkv = hkv; a.d = d;
   a.wait_limit_ns = 1000000000ull;
   return a;
@@ -87,7 +93,7 @@ int pa_paged_schedule(const int32_t* q_len, const int32_t* kv_len, int32_t B, in
   ScheduleArgs a;
   a.q_len = q_len; a.kv_len = kv_len; a.B = B;
   a.block_table = block_table; a.table_stride = table_stride; a.max_pages = max_pages;
-  a.free_pages = free_pages; a.n_free = n_free; a.page_size = page_size;
+  a.free_pages = free_pages; a.n_free = n_free; a.page_shift = log2_of(page_size);
   a.n_tokens = n_tokens;
   a.cu_q = cu_q; a.kv_len_out = kv_len_out; a.positions = positions; a.slots = slots; a.n_used = n_used;
   a.status = static_cast<DeviceStatus*>(ws);
@@ -164,6 +170,7 @@ int pa_prompt_attend(const void* q, const void* k, const void* v, int dtype, int
   rc = check_ws(ws, ws_bytes, plan_attend(a, N, nullptr));
   if (rc) return rc;
   plan_attend(a, N, ws);
+  if (static_cast<int64_t>(a.piece_cap) * hkv > INT32_MAX) return PA_ERR_UNSUPPORTED;   // blocks of one launch
   if (B == 0 || N == 0) return clear_status(ws, s);
   a.q = q; a.k = k; a.v = v;
   a.ldq = ldq; a.ldk = ldk; a.ldv = ldv;
@@ -207,6 +214,7 @@ int pa_paged_attend(const void* q, int dtype, int64_t N, int64_t ldq, const int3
   rc = check_ws(ws, ws_bytes, plan_attend(a, max_kv, nullptr));
   if (rc) return rc;
   plan_attend(a, max_kv, ws);
+  if (static_cast<int64_t>(a.piece_cap) * hkv > INT32_MAX) return PA_ERR_UNSUPPORTED;   // blocks of one launch
   if (B == 0 || N == 0) return clear_status(ws, s);
   a.q = q; a.k = k_pages; a.v = v_pages;
   a.ldq = ldq;

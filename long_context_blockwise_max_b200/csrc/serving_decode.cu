@@ -116,6 +116,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(AttendArg
   using C = DecCfg<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_wait();
+  grid_dep_launch();
   const int64_t total = a.head->decode_units;
   const int64_t each = total / gridDim.x, more = total % gridDim.x;
   auto first_unit = [&](int64_t c) { return c * each + (c < more ? c : more); };
@@ -445,8 +447,7 @@ int launch(const AttendArgs& a, cudaStream_t s) {
   static_assert(smem <= 232448, "shared memory of one block");
   if (cudaFuncSetAttribute(attend_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return PA_ERR_CUDA;
-  attend_decode_kernel<D><<<a.decode_ctas, kWarps * 32, smem, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return launch_overlapped(attend_decode_kernel<D>, dim3(a.decode_ctas), kWarps * 32, smem, s, a);
 }
 
 }  // namespace

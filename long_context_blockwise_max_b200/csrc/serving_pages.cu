@@ -12,38 +12,21 @@ __device__ __forceinline__ int32_t sat32(int64_t x) {
   return static_cast<int32_t>(x < INT32_MAX ? x : INT32_MAX);
 }
 
-// What request b asks for: its lengths, the pages it holds and needs.
-struct Request {
-  int64_t q, kv;
-  int64_t held, need;
-  bool fits, bad;
-};
-
-__device__ __forceinline__ Request request_of(const ScheduleArgs& a, int b) {
-  Request r;
-  r.q = a.q_len[b];
-  r.kv = a.kv_len[b];
-  r.bad = r.q < 0 || r.kv < 0;
-  if (r.q < 0) r.q = 0;
-  if (r.kv < 0) r.kv = 0;
-  r.held = (r.kv + a.page_size - 1) / a.page_size;
-  const int64_t all = (r.kv + r.q + a.page_size - 1) / a.page_size;
-  r.need = r.q > 0 ? all - r.held : 0;
-  r.fits = r.q == 0 || all <= a.max_pages;
-  return r;
-}
-
 // Two prefix sums over the requests (new tokens, new pages), then one entry
 // per token and per new page, each found by bisection in them.  Every block
-// builds the sums by itself (B is at most 8192: a few microseconds of loads
-// that hit L2), which saves a second launch and a grid-wide wait; tokens and
-// pages are spread over the blocks.
+// builds the sums by itself (B is at most 8192: a few loads per thread that
+// hit L2), which saves a second launch and a grid-wide wait; tokens and pages
+// are spread over the blocks.  Latency-bound: 64 requests take the time of
+// their loads, one scan and one look-up.
 __global__ void __launch_bounds__(1024) paged_schedule_kernel(ScheduleArgs a) {
   extern __shared__ int32_t sm[];
-  int32_t* cu = sm;                  // [B + 1]
-  int32_t* pages = sm + a.B + 1;     // [B + 1] pages asked for before request b
-  __shared__ int64_t tmp[33];
+  int32_t* cu = sm;                  // [B + 1] new tokens before request b
+  int32_t* pages = cu + a.B + 1;     // [B + 1] new pages asked for before it
+  int32_t* cached = pages + a.B + 1; // [B] tokens it has
+  uint8_t* granted = reinterpret_cast<uint8_t*>(cached + a.B);   // [B]
+  __shared__ int64_t tmp[2][64];
   __shared__ int32_t used;
+  const int shift = a.page_shift, page = 1 << shift;
   if (threadIdx.x == 0) {
     cu[0] = 0;
     pages[0] = 0;
@@ -52,24 +35,36 @@ __global__ void __launch_bounds__(1024) paged_schedule_kernel(ScheduleArgs a) {
   __syncthreads();
   const bool first = blockIdx.x == 0;
   int64_t tok_base = 0, page_base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 1024) {
+  for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
-    Request r = {};
-    r.fits = true;
-    if (b < a.B) r = request_of(a, b);
-    int64_t tok_all, page_all;
-    const int64_t toks = tok_base + block_incl_scan<int64_t>(r.q, tmp, &tok_all);
-    const int64_t pgs = page_base + block_incl_scan<int64_t>(r.fits ? r.need : 0, tmp, &page_all);
+    int64_t q = 0, kv = 0;
+    bool bad = false;
     if (b < a.B) {
+      q = a.q_len[b];
+      kv = a.kv_len[b];
+      bad = q < 0 || kv < 0;
+      q = q < 0 ? 0 : q;
+      kv = kv < 0 ? 0 : kv;
+    }
+    const int64_t held = (kv + page - 1) >> shift, all = (kv + q + page - 1) >> shift;
+    const int64_t need = q > 0 ? all - held : 0;
+    const bool fits = q == 0 || all <= a.max_pages;
+    int64_t toks = q, pgs = fits ? need : 0, tok_all, page_all;
+    block_incl_scan2<int64_t>(toks, pgs, tmp[(b0 / blockDim.x) & 1], &tok_all, &page_all);
+    toks += tok_base;
+    pgs += page_base;
+    if (b < a.B) {
+      const bool ok = fits && (need == 0 || pgs <= a.n_free);
       cu[b + 1] = sat32(toks);
       pages[b + 1] = sat32(pgs);
-      const bool granted = r.fits && (r.need == 0 || pgs <= a.n_free);
-      if (granted && r.need > 0) atomicMax(&used, sat32(pgs));
+      cached[b] = static_cast<int32_t>(kv);
+      granted[b] = ok;
+      if (ok && need > 0) atomicMax(&used, sat32(pgs));
       if (first) {
         a.cu_q[b + 1] = sat32(toks);
-        a.kv_len_out[b] = sat32(granted ? r.kv + r.q : r.kv);
-        if (r.bad) set_status(a.status, PA_ERR_INVALID, b);
-        else if (!granted) set_status(a.status, PA_ERR_CAPACITY, b);
+        a.kv_len_out[b] = sat32(ok ? kv + q : kv);
+        if (bad) set_status(a.status, PA_ERR_INVALID, b);
+        else if (!ok) set_status(a.status, PA_ERR_CAPACITY, b);
       }
     }
     tok_base += tok_all;
@@ -81,28 +76,26 @@ __global__ void __launch_bounds__(1024) paged_schedule_kernel(ScheduleArgs a) {
     *a.n_used = used;
     if (tok_base > a.n_tokens) set_status(a.status, PA_ERR_INVALID, a.B);
   }
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 1024;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 1024 + threadIdx.x;
+  auto held_of = [&](int b) { return (static_cast<int64_t>(cached[b]) + page - 1) >> shift; };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   // the new pages into their requests' rows
   for (int64_t x = id; x < used; x += step) {
     const int b = upper_index(pages, a.B + 1, static_cast<int32_t>(x));
-    const Request r = request_of(a, b);
-    a.block_table[b * a.table_stride + r.held + (x - pages[b])] = a.free_pages[x];
+    a.block_table[b * a.table_stride + held_of(b) + (x - pages[b])] = a.free_pages[x];
   }
   // a position and a slot for each token
   for (int64_t t = id; t < a.n_tokens; t += step) {
     int32_t pos = 0, slot = -1;
     if (t < cu[a.B]) {
       const int b = upper_index(cu, a.B + 1, static_cast<int32_t>(t));
-      const Request r = request_of(a, b);
-      const int64_t p = r.kv + (t - cu[b]);
+      const int64_t p = static_cast<int64_t>(cached[b]) + (t - cu[b]);
       pos = sat32(p);
-      if (r.fits && (r.need == 0 || pages[b + 1] <= a.n_free)) {
-        const int64_t i = p / a.page_size;
-        const int64_t page = i < r.held ? a.block_table[b * a.table_stride + i]
-                                        : a.free_pages[pages[b] + (i - r.held)];
-        const int64_t s = page * a.page_size + p % a.page_size;
-        if (page < 0 || s > INT32_MAX) set_status(a.status, PA_ERR_INVALID, b, static_cast<int>(page));
+      if (granted[b]) {
+        const int64_t i = p >> shift, held = held_of(b);
+        const int64_t pg = i < held ? a.block_table[b * a.table_stride + i] : a.free_pages[pages[b] + (i - held)];
+        const int64_t s = (pg << shift) + (p & (page - 1));
+        if (pg < 0 || s > INT32_MAX) set_status(a.status, PA_ERR_INVALID, b, static_cast<int>(pg));
         else slot = static_cast<int32_t>(s);
       }
     }
@@ -189,14 +182,18 @@ __global__ void __launch_bounds__(256) paged_append_kernel(AppendArgs a, RopeFre
 }  // namespace
 
 int launch_paged_schedule(const ScheduleArgs& a, cudaStream_t s) {
-  const size_t smem = sizeof(int32_t) * 2 * (static_cast<size_t>(a.B) + 1);
+  const size_t smem = 13 * static_cast<size_t>(a.B) + 8;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(paged_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return PA_ERR_CUDA;
-  const int64_t want = (a.n_tokens + 4095) / 4096;   // 4 tokens per thread before another block starts
+  // one thread per token up to a block per SM; a small step's block has no
+  // more threads than its requests and tokens need
+  const int64_t most = a.n_tokens > a.B ? a.n_tokens : a.B;
+  const int threads = most <= 256 ? 256 : 1024;
+  const int64_t want = (a.n_tokens + threads - 1) / threads;
   const int grid = static_cast<int>(want < 1 ? 1 : want > kSms ? kSms : want);
-  paged_schedule_kernel<<<grid, 1024, smem, s>>>(a);
+  paged_schedule_kernel<<<grid, threads, smem, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

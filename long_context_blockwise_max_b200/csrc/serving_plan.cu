@@ -16,14 +16,15 @@ namespace pa {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = 1024;
+constexpr int kBuckets = 256;
 // A piece's fixed cost (prologue, first copies in flight, epilogue) in key
-// tiles, and the most (rows, kv head) pairs for which cutting keys is
-// looked at: from three waves of blocks on there is nothing to gain.
-constexpr int kPieceCost = 7;
-constexpr int kCutBelow = 3 * kSms;
+// tiles.  Cutting keys is looked at while the rows give less than three waves
+// of blocks: from there on there is nothing to gain.
+constexpr int kPieceCost = 5;
 constexpr int kMaxCut = 64;
+constexpr int kMaxCutItems = 1024;
+// K and V of this many bytes stay in L2 (126 MB) beside q and o.
+constexpr double kL2Keys = 64e6;
 
 struct Lens {
   int64_t row0, q, kv;
@@ -61,28 +62,33 @@ __device__ __forceinline__ void put_piece(const AttendArgs& a, int at, int b, co
   dst[1] = make_int4(part, static_cast<int>(r.row0), static_cast<int>(r.q), static_cast<int>(r.kv));
 }
 
-__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(AttendArgs a, int64_t max_kv) {
+// One block.  Latency-bound (loads of the lengths, one scan, bisections in
+// shared memory): its time is on the critical path of every call.
+__global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t max_kv) {
+  grid_dep_launch();
   extern __shared__ __align__(16) uint8_t raw[];
-  int64_t* units = reinterpret_cast<int64_t*>(raw);          // [B + 1] decode key groups before request b
+  int64_t* units = reinterpret_cast<int64_t*>(raw);               // [B + 1] decode key groups before request b
   int32_t* items = reinterpret_cast<int32_t*>(units + a.B + 1);   // [B + 1] row groups before request b
-  __shared__ int64_t tmp[33];
+  __shared__ int64_t tmp[2][64];
   __shared__ int hist[kBuckets];
+  __shared__ int depth[kMaxCutItems], part_of[kMaxCutItems], first_piece[kMaxCutItems + 1];
   __shared__ int deepest, n_merge;
-  __shared__ unsigned long long best;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ unsigned long long best, keys;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   if (tid < static_cast<int>(kStatusBytes / 4)) reinterpret_cast<int32_t*>(a.status)[tid] = 0;
-  for (int c = tid; c < a.decode_ctas; c += kPlanThreads) a.done[c] = 0;
+  for (int c = tid; c < a.decode_ctas; c += threads) a.done[c] = 0;
+  if (tid < kBuckets) hist[tid] = 0;
   if (tid == 0) {
     units[0] = 0;
     items[0] = 0;
     deepest = 0;
     n_merge = 0;
     best = ~0ull;
+    keys = 0;
   }
-  for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
   __syncthreads();
   int64_t item_base = 0, unit_base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += threads) {
     const int b = b0 + tid;
     int64_t ni = 0, nu = 0;
     if (b < a.B) {
@@ -94,24 +100,25 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(AttendArgs a,
         } else {
           ni = (r.q + a.tile_tokens - 1) / a.tile_tokens;
           atomicMax(&deepest, static_cast<int>((keys_seen(r.kv, r.q, r.q) + kPlanTile - 1) / kPlanTile));
+          atomicAdd(&keys, static_cast<unsigned long long>(r.kv));
         }
       }
     }
-    int64_t all;
-    const int64_t xi = item_base + block_incl_scan<int64_t>(ni, tmp, &all);
-    item_base += all;
-    const int64_t xu = unit_base + block_incl_scan<int64_t>(nu, tmp, &all);
-    unit_base += all;
+    int64_t i_all, u_all;
+    block_incl_scan2<int64_t>(ni, nu, tmp[(b0 / threads) & 1], &i_all, &u_all);
     if (b < a.B) {
-      items[b + 1] = static_cast<int32_t>(xi < INT32_MAX ? xi : INT32_MAX);
-      units[b + 1] = xu;
+      const int64_t x = item_base + ni;
+      items[b + 1] = static_cast<int32_t>(x < INT32_MAX ? x : INT32_MAX);
+      units[b + 1] = unit_base + nu;
     }
+    item_base += i_all;
+    unit_base += u_all;
   }
   __syncthreads();
   // ---- decode: equal ranges of key groups, one per block ----------------
   if (a.decode_ctas > 0) {
     const int64_t each = unit_base / a.decode_ctas, more = unit_base % a.decode_ctas;
-    for (int c = tid; c < a.decode_ctas; c += kPlanThreads) {
+    for (int c = tid; c < a.decode_ctas; c += threads) {
       const int64_t u0 = c * each + (c < more ? c : more);
       DecodeStart st = {0, 0, 0, 0};
       if (u0 < unit_base) {
@@ -125,107 +132,142 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(AttendArgs a,
     }
   }
   // ---- tiles --------------------------------------------------------------
-  const int64_t most = a.piece_cap;
-  const int n = static_cast<int>(item_base < most ? item_base : most);
-  if (item_base > most && tid == 0) set_status(a.status, PA_ERR_INVALID, a.B);   // rows counted twice
-  bool cut = a.part_cap > 0 && n > 0 && static_cast<int64_t>(n) * a.hkv < kCutBelow && n <= kPlanThreads &&
-             n <= a.item_cap && deepest > 1;
-  int parts = 1, chunk = deepest;
-  if (cut) {
-    // the number of cuts of the deepest rows that ends first: blocks run in
-    // waves of one per SM, or, past one wave, fill the SMs evenly with half
-    // a piece of slack; a cut adds the merge of its partial results
-    for (int s = warp + 1; s <= kMaxCut; s += kPlanThreads / 32) {
-      const int c = (deepest + s - 1) / s;
-      int np = 0;
-      float load = 0.f;
-      for (int i = lane; i < n; i += 32) {
+  int n_pieces = 0;
+  if (a.tiles) {
+    const int64_t most = a.piece_cap;
+    const int n = static_cast<int>(item_base < most ? item_base : most);
+    if (item_base > most && tid == 0) set_status(a.status, PA_ERR_INVALID, a.B);   // rows counted twice
+    const int64_t blocks = static_cast<int64_t>(n) * a.hkv;
+    bool cut = a.part_cap > 0 && n > 0 && blocks < 3 * a.slots && n <= kMaxCutItems && deepest > 1;
+    int parts = 1;
+    if (cut) {
+      for (int i = tid; i < n; i += threads) {
+        const int b = upper_index(items, a.B + 1, i);
+        depth[i] = depth_of(lens_of(a, b, max_kv, false), (i - items[b]) * a.tile_tokens, a.tile_tokens);
+      }
+      __syncthreads();
+      // the number of cuts of the deepest rows that ends first: blocks run in
+      // waves of one per slot, or, past one wave, fill the slots evenly with
+      // half a piece of slack; a cut adds the merge of its partial results
+      for (int s = warp + 1; s <= kMaxCut && s <= deepest; s += threads / 32) {
+        const int c = (deepest + s - 1) / s;
+        int np = 0, cuts = 0;
+        float load = 0.f;
+        for (int i = lane; i < n; i += 32) {
+          const int d = depth[i], p = d > c ? (d + c - 1) / c : 1;
+          np += p;
+          cuts += p > 1 ? p : 0;
+          load += static_cast<float>(d) + kPieceCost * p;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          np += __shfl_xor_sync(0xffffffffu, np, o);
+          cuts += __shfl_xor_sync(0xffffffffu, cuts, o);
+          load += __shfl_xor_sync(0xffffffffu, load, o);
+        }
+        if (lane == 0 && cuts <= a.part_cap) {
+          float cost = static_cast<float>(kPieceCost + c);
+          if (static_cast<int64_t>(np) * a.hkv > a.slots)
+            cost = fmaxf(cost, load * a.hkv / a.slots + 0.5f * (kPieceCost + c));
+          if (s > 1) cost += 3.f + s / 8.f;
+          atomicMin(&best, (static_cast<unsigned long long>(__float_as_uint(cost)) << 32) | s);
+        }
+      }
+      __syncthreads();
+      if (best != ~0ull) parts = static_cast<int>(best & 0xffffffffu);
+      cut = parts > 1;
+    }
+    if (cut) {
+      // pieces and partial results by prefix sums over the rows, then one
+      // thread per piece
+      const int chunk = (deepest + parts - 1) / parts;
+      int n_parts = 0;
+      for (int i0 = 0; i0 < n; i0 += threads) {
+        const int i = i0 + tid;
+        int64_t p = 0;
+        if (i < n) p = depth[i] > chunk ? (depth[i] + chunk - 1) / chunk : 1;
+        int64_t at = p, slot = p > 1 ? p : 0, all, slots;
+        __syncthreads();
+        block_incl_scan2<int64_t>(at, slot, tmp[0], &all, &slots);
+        if (i < n) {
+          first_piece[i + 1] = n_pieces + static_cast<int>(at);
+          if (p > 1) {
+            const int first = n_parts + static_cast<int>(slot - p);
+            part_of[i] = first;
+            const int b = upper_index(items, a.B + 1, i);
+            const Lens r = lens_of(a, b, max_kv, false);
+            const int tok0 = (i - items[b]) * a.tile_tokens;
+            a.items[atomicAdd(&n_merge, 1)] = {
+                static_cast<int32_t>(r.row0) + tok0,
+                static_cast<int32_t>(min(static_cast<int64_t>(a.tile_tokens), r.q - tok0)), first,
+                static_cast<int32_t>(p)};
+          } else {
+            part_of[i] = -1;
+          }
+        }
+        n_pieces += static_cast<int>(all);
+        n_parts += static_cast<int>(slots);
+      }
+      if (tid == 0) first_piece[0] = 0;
+      __syncthreads();
+      for (int x = tid; x < n_pieces; x += threads) {
+        const int i = upper_index(first_piece, n + 1, x);
+        const int p = first_piece[i + 1] - first_piece[i], k = x - first_piece[i];
         const int b = upper_index(items, a.B + 1, i);
         const Lens r = lens_of(a, b, max_kv, false);
-        const int d = depth_of(r, (i - items[b]) * a.tile_tokens, a.tile_tokens);
-        const int p = d > c ? (d + c - 1) / c : 1;
-        np += p;
-        load += static_cast<float>(d) + kPieceCost * p;
+        const int lo = depth[i] / p, more = depth[i] % p;   // the first `more` pieces have a tile more
+        const int kt0 = k * lo + min(k, more);
+        put_piece(a, x, b, r, (i - items[b]) * a.tile_tokens, kt0, kt0 + lo + (k < more),
+                  part_of[i] < 0 ? -1 : part_of[i] + k);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        np += __shfl_xor_sync(0xffffffffu, np, o);
-        load += __shfl_xor_sync(0xffffffffu, load, o);
+    } else {
+      // deepest first: a counting sort by depth (the order inside a bucket is
+      // free; it changes no result).  One wave needs no order.
+      const bool sort = blocks > a.slots;
+      auto bucket = [&](int d) {
+        return deepest > 0 ? kBuckets - 1 - static_cast<int>(static_cast<int64_t>(d) * (kBuckets - 1) / deepest) : 0;
+      };
+      if (sort) {
+        for (int i = tid; i < n; i += threads) {
+          const int b = upper_index(items, a.B + 1, i);
+          atomicAdd(&hist[bucket(depth_of(lens_of(a, b, max_kv, false), (i - items[b]) * a.tile_tokens,
+                                          a.tile_tokens))], 1);
+        }
+        __syncthreads();
+        const int64_t h = tid < kBuckets ? hist[tid] : 0;
+        int64_t at = h, none = 0, all, none_all;
+        block_incl_scan2<int64_t>(at, none, tmp[0], &all, &none_all);
+        if (tid < kBuckets) hist[tid] = static_cast<int>(at - h);
+        __syncthreads();
       }
-      if (lane == 0 && np <= a.part_cap) {
-        float cost = static_cast<float>(kPieceCost + c);
-        if (static_cast<int64_t>(np) * a.hkv > kSms)
-          cost = fmaxf(cost, load * a.hkv / kSms + 0.5f * (kPieceCost + c));
-        if (s > 1) cost += 3.f + s / 8.f;
-        atomicMin(&best, (static_cast<unsigned long long>(__float_as_uint(cost)) << 32) | s);
+      for (int i = tid; i < n; i += threads) {
+        const int b = upper_index(items, a.B + 1, i);
+        const Lens r = lens_of(a, b, max_kv, false);
+        const int tok0 = (i - items[b]) * a.tile_tokens;
+        const int d = depth_of(r, tok0, a.tile_tokens);
+        put_piece(a, sort ? atomicAdd(&hist[bucket(d)], 1) : i, b, r, tok0, 0, d, -1);
       }
+      n_pieces = n;
     }
     __syncthreads();
-    if (best != ~0ull) parts = static_cast<int>(best & 0xffffffffu);
-    chunk = (deepest + parts - 1) / parts;
-    cut = parts > 1;
   }
-  int n_pieces = n;
-  if (cut) {
-    int b = 0, tok0 = 0, d = 0, p = 0;
-    Lens r = {};
-    if (tid < n) {
-      b = upper_index(items, a.B + 1, tid);
-      r = lens_of(a, b, max_kv, false);
-      tok0 = (tid - items[b]) * a.tile_tokens;
-      d = depth_of(r, tok0, a.tile_tokens);
-      p = d > chunk ? (d + chunk - 1) / chunk : 1;
-    }
-    int64_t all;
-    const int at = static_cast<int>(block_incl_scan<int64_t>(p, tmp, &all)) - p;
-    n_pieces = static_cast<int>(all);
-    for (int i = 0; i < p; ++i)
-      put_piece(a, at + i, b, r, tok0, static_cast<int>(static_cast<int64_t>(d) * i / p),
-                static_cast<int>(static_cast<int64_t>(d) * (i + 1) / p), p > 1 ? at + i : -1);
-    if (p > 1) {
-      const int k = atomicAdd(&n_merge, 1);
-      a.items[k] = {static_cast<int32_t>(r.row0) + tok0,
-                    static_cast<int32_t>(min(static_cast<int64_t>(a.tile_tokens), r.q - tok0)), at, p};
-    }
-  } else {
-    // deepest first: a counting sort by depth (the order inside a bucket is
-    // free; it changes no result)
-    auto bucket = [&](int d) {
-      return deepest > 0 ? kBuckets - 1 - static_cast<int>(static_cast<int64_t>(d) * (kBuckets - 1) / deepest) : 0;
-    };
-    for (int i = tid; i < n; i += kPlanThreads) {
-      const int b = upper_index(items, a.B + 1, i);
-      atomicAdd(&hist[bucket(depth_of(lens_of(a, b, max_kv, false), (i - items[b]) * a.tile_tokens,
-                                      a.tile_tokens))], 1);
-    }
-    __syncthreads();
-    const int h = hist[tid];
-    int64_t all;
-    const int before = static_cast<int>(block_incl_scan<int64_t>(h, tmp, &all)) - h;
-    hist[tid] = before;
-    __syncthreads();
-    for (int i = tid; i < n; i += kPlanThreads) {
-      const int b = upper_index(items, a.B + 1, i);
-      const Lens r = lens_of(a, b, max_kv, false);
-      const int tok0 = (i - items[b]) * a.tile_tokens;
-      const int d = depth_of(r, tok0, a.tile_tokens);
-      put_piece(a, atomicAdd(&hist[bucket(d)], 1), b, r, tok0, 0, d, -1);
-    }
-  }
-  __syncthreads();
   if (tid == 0) {
     a.head->n_pieces = n_pieces;
     a.head->n_items = n_merge;
     a.head->abort = 0;
+    a.head->heads_inner = static_cast<double>(keys) * a.hkv * a.d * (a.dtype == PA_BF16 ? 4 : 8) <= kL2Keys;
     a.head->decode_units = unit_base;
   }
 }
 
 // Rows cut into pieces: lse = ln sum_p exp(lse_p), o = sum_p exp(lse_p - lse) o_p,
-// in piece order.  One warp per row.
+// in piece order.  One warp per row; the partial rows' loads are independent
+// and go out several at a time.
 template <typename OT, int D>
 __global__ void __launch_bounds__(256) attend_merge_kernel(AttendArgs a) {
-  constexpr int VPL = D / 32;
+  constexpr int VPL = D / 32, U = 16 / VPL;   // elements of a lane, parts in flight
+  using Vec = std::conditional_t<VPL == 4, float4, float2>;
+  grid_dep_wait();
   if (static_cast<int>(blockIdx.x) >= a.head->n_items) return;
   const MergeItem it = a.items[blockIdx.x];
   const int kvh = blockIdx.y, g = a.hq / a.hkv;
@@ -235,54 +277,72 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(AttendArgs a) {
   const int64_t base = (static_cast<int64_t>(it.part0) * a.hkv + kvh) * a.tile_rows;
   for (int r = blockIdx.z * 8 + warp; r < rows; r += gridDim.z * 8) {
     const float* ls = a.part_lse + base + r;
+    const Vec* src = reinterpret_cast<const Vec*>(a.part_o + (base + r) * D) + lane;
     float m = -INFINITY;
     for (int p = lane; p < it.n_parts; p += 32) m = fmaxf(m, ls[p * step]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float sub = m == -INFINITY ? 0.f : m;   // a NaN stays one
     float z = 0.f;
-    for (int p = lane; p < it.n_parts; p += 32) z += expf(ls[p * step] - sub);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     float acc[VPL] = {};
-    const float* src = a.part_o + (base + r) * D + lane * VPL;
-    if (z != 0.f) {
-      const float inv = 1.f / z;
-#pragma unroll 4
-      for (int p = 0; p < it.n_parts; ++p) {
-        const float w = expf(ls[p * step] - sub) * inv;
-        if (w == 0.f) continue;   // a piece without a visible key
+    for (int p0 = 0; p0 < it.n_parts; p0 += 32) {
+      const float w = p0 + lane < it.n_parts ? expf(ls[(p0 + lane) * step] - sub) : 0.f;
+      z += w;
+      const int n = min(32, it.n_parts - p0);
+      for (int p = 0; p < n; p += U) {
+        Vec v[U];
 #pragma unroll
-        for (int e = 0; e < VPL; ++e) acc[e] += w * src[p * step * D + e];
+        for (int k = 0; k < U; ++k)
+          if (p + k < n) v[k] = src[(p0 + p + k) * step * (D / VPL)];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, (p + k) & 31);
+          if (p + k >= n || wk == 0.f) continue;   // (a piece without a visible key)
+          const float* x = reinterpret_cast<const float*>(&v[k]);
+#pragma unroll
+          for (int e = 0; e < VPL; ++e) acc[e] += wk * x[e];
+        }
       }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    const float inv = z == 0.f ? 0.f : 1.f / z;
     const int64_t row = static_cast<int64_t>(it.row0) + r / g;
     const int head = kvh * g + r % g;
     OT* dst = static_cast<OT*>(a.o) + (row * a.hq + head) * D + lane * VPL;
 #pragma unroll
-    for (int e = 0; e < VPL; ++e) dst[e] = from_f32<OT>(acc[e]);
+    for (int e = 0; e < VPL; ++e) dst[e] = from_f32<OT>(acc[e] * inv);
     if (lane == 0 && a.lse) a.lse[row * a.hq + head] = z == 0.f ? -INFINITY : sub + logf(z);
   }
 }
 
 template <typename OT>
-void merge(const AttendArgs& a, cudaStream_t s) {
-  const dim3 grid(a.item_cap, a.hkv, (a.tile_rows + 31) / 32);
-  if (a.d == 128) attend_merge_kernel<OT, 128><<<grid, 256, 0, s>>>(a);
-  else attend_merge_kernel<OT, 64><<<grid, 256, 0, s>>>(a);
+int merge(const AttendArgs& a, cudaStream_t s) {
+  // about eight waves of eight warps; a block takes several rows when there are more
+  const int most = (a.tile_rows + 7) / 8, fill = 8 * kSms / (a.item_cap * a.hkv) + 1;
+  const dim3 grid(a.item_cap, a.hkv, most < fill ? most : fill);
+  return launch_overlapped(a.d == 128 ? attend_merge_kernel<OT, 128> : attend_merge_kernel<OT, 64>, grid, 256, 0, s, a);
 }
 
 }  // namespace
+
+// few requests and rows and nothing to cut: the fewer warps at its barriers, the
+// sooner it ends
+static int plan_threads(const AttendArgs& a) {
+  return a.B <= 256 && a.piece_cap <= 1024 && a.part_cap == 0 ? 256 : 1024;
+}
 
 size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws) {
   const int g = a.hq / a.hkv;
   if (a.dtype == PA_BF16) {
     a.tile_rows = 256;                // two tiles of 128 rows
     a.tile_tokens = 2 * (128 / g);
+    a.slots = kSms;
   } else {
     // fp32 rows per block: 16 when no request has more, 64 otherwise
     a.tile_rows = a.max_q > 0 && static_cast<int64_t>(a.max_q) * g <= 16 ? 16 : 64;
     a.tile_tokens = a.tile_rows / g;
+    a.slots = simt_blocks_per_sm(a) * kSms;
   }
   // Rows per kv head up to which a request is the decode kernel's.  A call
   // whose requests are long on average leaves them all to the tile kernel:
@@ -298,12 +358,13 @@ size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws) {
   const int64_t deep = (max_kv + kPlanTile - 1) / kPlanTile;
   a.part_cap = 0;
   a.item_cap = 0;
-  if (a.tiles && full * a.hkv < kCutBelow && 2 * kSms / a.hkv >= 2 && deep > 1) {
+  const int64_t cuts = 2 * a.slots / a.hkv;   // partial results per kv head: two waves of blocks
+  if (a.tiles && full * a.hkv < 3 * a.slots && cuts >= 2 && deep > 1) {
     const int64_t most = groups * deep;
-    a.part_cap = static_cast<int>(most < 2 * kSms / a.hkv ? most : 2 * kSms / a.hkv);
-    a.item_cap = static_cast<int>(groups < a.part_cap ? groups : a.part_cap);
+    a.part_cap = static_cast<int>(most < cuts ? most : cuts);
+    a.item_cap = static_cast<int>(groups < a.part_cap ? groups : a.part_cap);   // rows that are cut
   }
-  a.piece_cap = static_cast<int>(groups > a.part_cap ? groups : a.part_cap);
+  a.piece_cap = static_cast<int>(groups + a.part_cap);
   char* w = static_cast<char*>(ws);
   size_t off = 0;
   auto take = [&](auto*& p, size_t count) {
@@ -328,22 +389,19 @@ size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws) {
 int launch_attend(const AttendArgs& a, cudaStream_t s) {
   const int64_t max_kv = a.block_table ? static_cast<int64_t>(a.max_pages) * a.page_size : a.N;
   const size_t smem = (sizeof(int64_t) + sizeof(int32_t)) * (static_cast<size_t>(a.B) + 1);
-  if (smem > 40 * 1024 &&
+  if (smem > 32 * 1024 &&   // beside 14 KB of static arrays
       cudaFuncSetAttribute(attend_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return PA_ERR_CUDA;
-  attend_plan_kernel<<<1, kPlanThreads, smem, s>>>(a, max_kv);
-  profile_begin(s);
+  attend_plan_kernel<<<1, plan_threads(a), smem, s>>>(a, max_kv);
+  if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
   int rc = PA_OK;
+  profile_begin(s);
   if (a.decode_ctas > 0) rc = launch_attend_decode(a, s);
   if (rc == PA_OK && a.tiles) rc = a.dtype == PA_BF16 ? launch_attend_tc(a, s) : launch_attend_simt(a, s);
   profile_end(s);
-  if (rc != PA_OK) return rc;
-  if (a.part_cap > 0) {
-    if (a.dtype == PA_F32) merge<float>(a, s);
-    else merge<__nv_bfloat16>(a, s);
-  }
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (rc == PA_OK && a.part_cap > 0) rc = a.dtype == PA_F32 ? merge<float>(a, s) : merge<__nv_bfloat16>(a, s);
+  return rc;
 }
 
 }  // namespace pa

@@ -36,9 +36,12 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
   float* sv = sm + C::OFF_V;
   float* sp = sm + C::OFF_P;
   int64_t* slot = reinterpret_cast<int64_t*>(sm + C::FLOATS);
-  if (static_cast<int>(blockIdx.x) >= a.head->n_pieces) return;
-  const Piece pc = a.pieces[blockIdx.x];
-  const int kvh = blockIdx.y, g = a.hq / a.hkv;
+  grid_dep_wait();
+  grid_dep_launch();
+  int at, kvh;
+  if (!piece_of_block(a, &at, &kvh)) return;
+  const Piece pc = a.pieces[at];
+  const int g = a.hq / a.hkv;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int n_rows = min(a.tile_tokens, pc.q_len - pc.tok0) * g;
   const float scale = static_cast<float>(kLog2e / sqrt(static_cast<double>(D)));
@@ -193,8 +196,7 @@ int launch(const AttendArgs& a, cudaStream_t s) {
   if (cudaFuncSetAttribute(attend_simt_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
     return PA_ERR_CUDA;
-  attend_simt_kernel<T, D, ROWS><<<dim3(a.piece_cap, a.hkv), 256, smem, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return launch_overlapped(attend_simt_kernel<T, D, ROWS>, dim3(tile_blocks(a)), 256, smem, s, a);
 }
 
 template <typename T>
@@ -205,8 +207,14 @@ int launch_t(const AttendArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int launch_attend_simt(const AttendArgs& a, cudaStream_t s) {
-  return a.dtype == PA_F32 ? launch_t<float>(a, s) : launch_t<__nv_bfloat16>(a, s);
+// by shared memory (228 KB per SM) and registers (128 a thread)
+int simt_blocks_per_sm(const AttendArgs& a) {
+  const int smem = a.tile_rows == 16 ? (a.d == 128 ? SimtCfg<128, 16>::SMEM : SimtCfg<64, 16>::SMEM)
+                                     : (a.d == 128 ? SimtCfg<128, 64>::SMEM : SimtCfg<64, 64>::SMEM);
+  const int n = 228 * 1024 / (smem + 1024);
+  return n < 2 ? n : 2;
 }
+
+int launch_attend_simt(const AttendArgs& a, cudaStream_t s) { return launch_t<float>(a, s); }
 
 }  // namespace pa

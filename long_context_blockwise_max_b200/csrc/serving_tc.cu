@@ -138,7 +138,6 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
                                                            const __grid_constant__ SvParams p) {
   using C = SvCfg<D>;
   const AttendArgs& a = p.a;
-  if (static_cast<int>(blockIdx.x) >= a.head->n_pieces) return;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   SvBars* bars = reinterpret_cast<SvBars*>(smem + C::OFF_BAR);
@@ -170,14 +169,26 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
-  const Piece pc = a.pieces[blockIdx.x];
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  grid_dep_wait();      // the set-up above overlaps the plan
+  grid_dep_launch();
+  int at, kvh;
+  if (!piece_of_block(a, &at, &kvh)) {
+    if (warp == 2) tmem_dealloc(tmem, 512);
+    return;
+  }
+  const Piece pc = a.pieces[at];
   volatile int* abort = &bars->abort;
   volatile int* gabort = &a.head->abort;
-  const int kvh = blockIdx.y, g = a.hq / a.hkv;
+  const int g = a.hq / a.hkv;
   const int tpt = 128 / g;                           // tokens per row tile
   const int ctx = pc.kv_len - pc.q_len;              // position of the first new token (may be negative)
   const int n = pc.kt1 - pc.kt0;                     // key tiles of this piece
@@ -218,9 +229,6 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
     };
     int row = n > 0 ? row_of(pc.kt0) : 0;
     if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
       const int qt = two ? 2 : 1;
       const int q_bytes = tpt * g * 128 * C::NKB;
       mbar_arrive_expect_tx(&bars->q_full, qt * q_bytes);
@@ -372,7 +380,8 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       fence_async_smem();
       mbar_arrive(&bars->v_ready[st]);
     }
-    bar_arrive<1, 320>();
+    bar_arrive<1, 192>();   // one barrier per softmax warpgroup: neither waits for the other here
+    bar_arrive<2, 192>();
   } else {
     // -------------------------------------------------------------- softmax
     const int t = warp >= 8 ? 1 : 0;
@@ -459,7 +468,8 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       tc_fence_before();
       mbar_arrive(&bars->p_full[t]);
     }
-    bar_sync<1, 320>();   // the guard's notes are complete
+    if (t == 0) bar_sync<1, 192>();   // the guard's notes are complete
+    else bar_sync<2, 192>();
     // Rows' final maximum and sum.  Weights w0, w1 of the two O's (one row
     // tile) or w0 of its own (two).
     const int n_other = nt[t ^ 1];
@@ -475,7 +485,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
     if (!two) {
       bars->ml[t][0][rl] = m_run;
       bars->ml[t][1][rl] = l_run;
-      bar_sync<2, 256>();
+      bar_sync<3, 256>();
       const float m2 = bars->ml[t ^ 1][0][rl], l2 = bars->ml[t ^ 1][1][rl];
       const float m = fmaxf(m_run, m2);
       if (m != -INFINITY) {
@@ -501,30 +511,19 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       // (every QK^T has been read by now)
       uint8_t* stage = sQ + (warp - 4) * 32 * D * 2;
       const int64_t prow = (static_cast<int64_t>(pc.part) * a.hkv + kvh) * a.tile_rows + (two ? t * tpt * g : 0) + rl;
-      for (int ci = 0; ci < nc; ++ci) {
-        const int c = c0 + ci;
-        float v[32];
-        uint32_t ov[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = 0.f;
-        if (my > 0) {
-          tmem_ld_x32(o_tmem + 32 * c, ov);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = empty ? 0.f : __uint_as_float(ov[e]) * w_own;
-        }
-        if (!two && n_other > 0) {
-          tmem_ld_x32(o_oth + 32 * c, ov);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] += empty ? 0.f : __uint_as_float(ov[e]) * w_oth;
-        }
+      // columns 32 c .. 32 c + 31 of this thread's row
+      auto emit = [&](int c, float (&v)[32]) {
         if (odd) {
-#pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int col = 32 * c + e;
             const bool pos = bars->first[0][col] <= lim, neg = bars->first[1][col] <= lim;
-            if (bars->first[2][col] <= lim || (pos && neg)) v[e] = __int_as_float(0x7fc00000);
-            else if (pos) v[e] += INFINITY;
-            else if (neg) v[e] -= INFINITY;
+            float add = 0.f;
+            if (bars->first[2][col] <= lim || (pos && neg)) add = __int_as_float(0x7fc00000);
+            else if (pos) add = INFINITY;
+            else if (neg) add = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (k == e) v[k] += add;
           }
         }
         if (pc.part >= 0) {
@@ -542,6 +541,35 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
                            pack2(v[8 * e + 4], v[8 * e + 5]), pack2(v[8 * e + 6], v[8 * e + 7]));
           }
         }
+      };
+      if (two && my > 0) {
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+          uint32_t ov[32];
+          float v[32];
+          tmem_ld_x32(o_tmem + 32 * c, ov);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = empty ? 0.f : __uint_as_float(ov[e]) * w_own;
+          emit(c, v);
+        }
+      } else {
+        for (int c = c0; c < c0 + nc; ++c) {
+          uint32_t ov[32];
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.f;
+          if (my > 0) {
+            tmem_ld_x32(o_tmem + 32 * c, ov);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = empty ? 0.f : __uint_as_float(ov[e]) * w_own;
+          }
+          if (!two && n_other > 0) {
+            tmem_ld_x32(o_oth + 32 * c, ov);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] += empty ? 0.f : __uint_as_float(ov[e]) * w_oth;
+          }
+          emit(c, v);
+        }
       }
       if (pc.part >= 0) {
         if (valid && (two || t == 0)) a.part_lse[prow] = lse;
@@ -551,14 +579,18 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
         __syncwarp();
         const int per = 4 * nc;           // 16-byte chunks of a row here: a power of two
         const int rows_per = 32 / per;    // rows per store of the warp
-        for (int r = lane / per; r < 32; r += rows_per) {
-          const int row = sub * 32 + r, rt = tok_t + row / g;
-          if (row >= tpt * g || rt >= pc.q_len) continue;
-          const int ch = 4 * c0 + lane % per;
+        const uint32_t ginv = 65536u / g + 1;   // row / g for rows below 128, g <= 64: exact
+        const int ch = 4 * c0 + lane % per, r0 = lane / per;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) +
+                             (static_cast<int64_t>(pc.row0) * a.hq + kvh * g) * D + 8 * ch;
+        const int last = min(tpt * g, (pc.q_len - tok_t) * g);   // rows of this tile
+#pragma unroll 4
+        for (int k = 0; k < per; ++k) {
+          const int r = r0 + k * rows_per, row = sub * 32 + r;
           const uint4 x = *reinterpret_cast<const uint4*>(stage + r * D * 2 + ((ch ^ (r & 7)) << 4));
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) +
-                               ((static_cast<int64_t>(pc.row0) + rt) * a.hq + kvh * g + row % g) * D + 8 * ch;
-          *reinterpret_cast<uint4*>(dst) = x;
+          const int tk = static_cast<int>((row * ginv) >> 16);
+          if (row < last)
+            *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(tok_t + tk) * a.hq + (row - tk * g)) * D) = x;
         }
       }
     }
@@ -614,8 +646,7 @@ int launch_tc(const AttendArgs& a, cudaStream_t s) {
   if (cudaFuncSetAttribute(attend_tc_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
       cudaSuccess)
     return PA_ERR_CUDA;
-  attend_tc_kernel<D, PAGED><<<dim3(a.piece_cap, a.hkv), 384, C::SMEM_BYTES, s>>>(mq, mk, mv, p);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return launch_overlapped(attend_tc_kernel<D, PAGED>, dim3(tile_blocks(a)), 384, C::SMEM_BYTES, s, mq, mk, mv, p);
 }
 
 }  // namespace

@@ -18,11 +18,12 @@ device and its current stream.  No call waits for the GPU (unless
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 
 import torch
 
 from . import pulsar
-from .pulsar import PulsarError, _check, _dtype_code, _lib, _need, _same
+from .pulsar import _check, _dtype_code, _lib, _need, _same
 
 # Every symbol declared in include/pulsar_serving.h.
 ABI_SYMBOLS = (
@@ -114,21 +115,21 @@ def _table(t: torch.Tensor, B: int):
 
 def _ws(nbytes: int, ref: torch.Tensor, ws):
     if ws is None:
-        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=ref.device)
+        return torch.empty(nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=ref.device)
     if not ws.is_contiguous():
         raise ValueError("ws: must be contiguous")
     return ws
 
 
-def _call(name: str, ref: torch.Tensor, ws, *args):
+def _call(fn, ref: torch.Tensor, ws, *args):
     """The C entry point on ``ref``'s device and that device's current stream."""
     dev = ref.device.index
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _call(name, ref, ws, *args)
-    rc = getattr(_lib, name)(*args, ws.data_ptr(), ws.numel() * ws.element_size(),
-                             torch.cuda.current_stream().cuda_stream)
-    _check(rc, name, ws)
+            return _call(fn, ref, ws, *args)
+    rc = fn(*args, ws.data_ptr(), ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0 or pulsar._STATUS_CHECKS:
+        _check(rc, fn.__name__, ws)
 
 
 def pa_paged_schedule(q_len, kv_len, block_table, free_pages, page_size: int, n_tokens: int, cu_q=None,
@@ -143,19 +144,19 @@ def pa_paged_schedule(q_len, kv_len, block_table, free_pages, page_size: int, n_
     _ints((("q_len", q_len), ("kv_len", kv_len), ("kv_len_out", kv_len_out)), B)
     stride = _table(block_table, B)
     _ints((("free_pages", free_pages),), 0)
-    new = lambda n: torch.empty(n, dtype=torch.int32, device=q_len.device)
     _ints((("cu_q", cu_q),), B + 1)
     _ints((("positions", positions), ("slots", slots)), n_tokens)
     _ints((("n_used", n_used),), 1)
     if kv_len_out is not None and kv_len_out.data_ptr() == kv_len.data_ptr() and B > 0:
         raise ValueError("kv_len_out: must not be kv_len")
-    cu_q = new(B + 1) if cu_q is None else cu_q
-    kv_len_out = new(B) if kv_len_out is None else kv_len_out
-    positions = new(n_tokens) if positions is None else positions
-    slots = new(n_tokens) if slots is None else slots
-    n_used = new(1) if n_used is None else n_used
+    given = (cu_q, kv_len_out, positions, slots, n_used)
+    sizes = (B + 1, B, n_tokens, n_tokens, 1)
+    if any(t is None for t in given):   # one allocation for those that are missing
+        own = torch.empty(sum(n for n, t in zip(sizes, given) if t is None), dtype=torch.int32, device=q_len.device)
+        own = iter(own.split([n for n, t in zip(sizes, given) if t is None]))
+        cu_q, kv_len_out, positions, slots, n_used = (next(own) if t is None else t for t in given)
     ws = _ws(256, q_len, ws)
-    _call("pa_paged_schedule", q_len, ws, _p(q_len), _p(kv_len), B, _p(block_table), stride, block_table.shape[1],
+    _call(_lib.pa_paged_schedule, q_len, ws, _p(q_len), _p(kv_len), B, _p(block_table), stride, block_table.shape[1],
           _p(free_pages), free_pages.numel(), int(page_size), n_tokens, _p(cu_q), _p(kv_len_out), _p(positions),
           _p(slots), _p(n_used))
     return cu_q, kv_len_out, positions, slots, n_used, ws
@@ -209,7 +210,8 @@ def pa_paged_append(q, k_new, v_new, positions, slots, k_pages, v_pages, rope_th
         raise ValueError("positions: needed to rotate")
     _need(q_out, "q_out", k_new.dtype, N * hq * d)
     _need(k_out, "k_out", k_new.dtype, N * hkv * d)
-    _dense(("q_out", q_out), ("k_out", k_out))
+    if q_out is not None or k_out is not None:
+        _dense(("q_out", q_out), ("k_out", k_out))
     for name, out, src, ld in (("q_out", q_out, q, ldq), ("k_out", k_out, k_new, ldk)):
         if out is not None and src is not None and out.data_ptr() == src.data_ptr() and N > 1 \
                 and ld != src.shape[1] * d:
@@ -219,7 +221,7 @@ def pa_paged_append(q, k_new, v_new, positions, slots, k_pages, v_pages, rope_th
     if k_out is None and want_k:
         k_out = torch.empty((N, hkv, d), dtype=k_new.dtype, device=k_new.device)
     ws = _ws(256, k_new, ws)
-    _call("pa_paged_append", k_new, ws, _p(q), _p(k_new), _p(v_new), _dtype_code(k_new), N, ldq, ldk, ldv, hq, hkv,
+    _call(_lib.pa_paged_append, k_new, ws, _p(q), _p(k_new), _p(v_new), _dtype_code(k_new), N, ldq, ldk, ldv, hq, hkv,
           d, float(rope_theta), _p(positions), _p(slots), _p(k_pages), _p(v_pages), n_slots, _p(q_out), _p(k_out))
     return q_out, k_out, ws
 
@@ -241,6 +243,7 @@ def _batch(cu_q):
     return cu_q.numel() - 1
 
 
+@lru_cache(maxsize=4096)   # a pure function of sizes
 def pa_prompt_attend_workspace_size(B, N, hq, hkv, d, dtype) -> int:
     return _lib.pa_prompt_attend_workspace_size(B, N, hq, hkv, d, dtype)
 
@@ -260,13 +263,14 @@ def pa_prompt_attend(q, k, v, cu_q, o=None, lse=None, want_lse: bool = True, ws=
     hkv, B, dt = k.shape[1], _batch(cu_q), _dtype_code(q)
     o, lse = _attend_outputs(q, o, lse, want_lse)
     if ws is None:
-        ws = _ws(_lib.pa_prompt_attend_workspace_size(B, N, hq, hkv, d, dt), q, None)
+        ws = _ws(pa_prompt_attend_workspace_size(B, N, hq, hkv, d, dt), q, None)
     ws = _ws(0, q, ws)
-    _call("pa_prompt_attend", q, ws, _p(q), _p(k), _p(v), dt, N, ldq, ldk, ldv, _p(cu_q), B, hq, hkv, d, _p(o),
+    _call(_lib.pa_prompt_attend, q, ws, _p(q), _p(k), _p(v), dt, N, ldq, ldk, ldv, _p(cu_q), B, hq, hkv, d, _p(o),
           _p(lse))
     return o, lse, ws
 
 
+@lru_cache(maxsize=4096)
 def pa_paged_attend_workspace_size(B, N, max_q, max_pages, page_size, hq, hkv, d, dtype) -> int:
     return _lib.pa_paged_attend_workspace_size(B, N, max_q, max_pages, page_size, hq, hkv, d, dtype)
 
@@ -289,9 +293,9 @@ def pa_paged_attend(q, cu_q, kv_len, block_table, k_pages, v_pages, max_q: int, 
     n_pages, page_size, hkv, _ = k_pages.shape
     o, lse = _attend_outputs(q, o, lse, want_lse)
     if ws is None:
-        ws = _ws(_lib.pa_paged_attend_workspace_size(B, N, int(max_q), block_table.shape[1], page_size, hq, hkv, d,
-                                                     dt), q, None)
+        ws = _ws(pa_paged_attend_workspace_size(B, N, int(max_q), block_table.shape[1], page_size, hq, hkv, d, dt),
+                 q, None)
     ws = _ws(0, q, ws)
-    _call("pa_paged_attend", q, ws, _p(q), dt, N, ldq, _p(cu_q), _p(kv_len), B, int(max_q), _p(block_table), stride,
+    _call(_lib.pa_paged_attend, q, ws, _p(q), dt, N, ldq, _p(cu_q), _p(kv_len), B, int(max_q), _p(block_table), stride,
           block_table.shape[1], page_size, _p(k_pages), _p(v_pages), n_pages, hq, hkv, d, _p(o), _p(lse))
     return o, lse, ws
