@@ -68,7 +68,9 @@ struct PlanHead {
   int32_t n_pieces;     // pieces of the tile kernels, per kv head
   int32_t n_items;      // entries of the merge list
   int32_t abort;        // a bounded wait ran out somewhere
-  int32_t heads_inner;  // order of the tile kernels' blocks (piece_of_block)
+  int32_t heads_inner;  // order of the tile kernels' work (piece_at)
+  uint32_t next;        // units of work taken beyond each block's first
+  int32_t pad;
   int64_t decode_units; // key groups of the decode kernel, over kv heads
 };
 
@@ -146,27 +148,25 @@ int launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// Blocks of a tile kernel: the most pieces the arguments allow, times kv heads.
+// Units of work of a tile kernel: the most pieces the arguments allow, times kv heads.
 inline unsigned tile_blocks(const AttendArgs& a) {
   return static_cast<unsigned>(a.piece_cap) * static_cast<unsigned>(a.hkv);
 }
 
 #ifdef __CUDACC__
-// Piece and kv head of this block; false if there is none.  Blocks that run
-// together share one kv head's K and V (which then stay in L2 however long
-// the caches are), or, when all of K and V fit there anyway, take the deepest
-// pieces of every head first, so that the launch ends with short ones.
-__device__ __forceinline__ bool piece_of_block(const AttendArgs& a, int* at, int* kvh) {
-  const unsigned n = static_cast<unsigned>(a.head->n_pieces), i = blockIdx.x;
-  if (i >= n * static_cast<unsigned>(a.hkv)) return false;
+// Piece and kv head of the i-th unit of work (of n_pieces * hkv).  Units that
+// run together share one kv head's K and V (which then stay in L2 however
+// long the caches are), or, when all of K and V fit there anyway, are the
+// deepest pieces of every head first, so that the launch ends with short ones.
+__device__ __forceinline__ void piece_at(const AttendArgs& a, unsigned i, int* at, int* kvh) {
+  const unsigned n = static_cast<unsigned>(a.head->n_pieces), h = static_cast<unsigned>(a.hkv);
   if (a.head->heads_inner) {
-    *at = static_cast<int>(i / static_cast<unsigned>(a.hkv));
-    *kvh = static_cast<int>(i % static_cast<unsigned>(a.hkv));
+    *at = static_cast<int>(i / h);
+    *kvh = static_cast<int>(i % h);
   } else {
     *at = static_cast<int>(i % n);
     *kvh = static_cast<int>(i / n);
   }
-  return true;
 }
 
 // Waits until the kernels before this one in the stream have ended and their

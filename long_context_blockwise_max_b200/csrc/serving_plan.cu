@@ -255,6 +255,7 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     a.head->n_pieces = n_pieces;
     a.head->n_items = n_merge;
     a.head->abort = 0;
+    a.head->next = 0;
     a.head->heads_inner = static_cast<double>(keys) * a.hkv * a.d * (a.dtype == PA_BF16 ? 4 : 8) <= kL2Keys;
     a.head->decode_units = unit_base;
   }

@@ -39,7 +39,8 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   int at, kvh;
-  if (!piece_of_block(a, &at, &kvh)) return;
+  if (blockIdx.x >= static_cast<unsigned>(a.head->n_pieces) * static_cast<unsigned>(a.hkv)) return;
+  piece_at(a, blockIdx.x, &at, &kvh);
   const Piece pc = a.pieces[at];
   const int g = a.hq / a.hkv;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;

@@ -1,13 +1,15 @@
 // Causal attention of packed prompts, and of new tokens over a paged cache,
 // on the sm_100a tensor cores (tcgen05 + TMEM + TMA), bf16.
 //
-// A block takes one piece of the plan (serving_plan.cu) for one kv head: up
-// to two tiles of 128 packed rows (a tile holds 128 / g tokens x the g query
-// heads of the group, so every K / V tile serves all of them and a request's
-// ragged end wastes less than one tile) against 128-key tiles.  12 warps:
-//   warp 0      TMA producer: Q once, then K / V tiles through 2-stage
-//               rings.  Packed rows are one box per 64 columns; a paged tile
-//               is one box per page, issued by as many lanes.
+// One block per SM walks the plan's pieces (serving_plan.cu), each for one kv
+// head: up to two tiles of 128 packed rows (a tile holds 128 / g tokens x the g
+// query heads of the group, so every K / V tile serves all of them and a
+// request's ragged end wastes less than one tile) against 128-key tiles.  12
+// warps, each walking the same pieces on its own:
+//   warp 0      TMA producer: Q of a piece, then K / V tiles through 2-stage
+//               rings that run on across pieces.  Packed rows are one box per
+//               64 columns; a paged tile is one box per page, issued by as
+//               many lanes.
 //   warp 1      MMA issuer (one thread): S = Q K^T (bf16 x bf16 -> fp32 in
 //               TMEM, exact products) and O += P V (P bf16 from TMEM).
 //   warps 2-3   guard of V tiles that hold masked keys (below); warp 2 also
@@ -21,6 +23,10 @@
 // rows, each with its own maximum, sum and O, joined at the end, so a short
 // query streams its keys at the same rate per block.
 //
+// The next piece's Q, first keys and first scores are under way while the
+// softmax warps store a piece's output: one block per piece took 8 us of
+// set-up and output per piece beside 2.1 us per key tile.
+//
 // Guard: P is zero at a masked key, but zero times an infinity or NaN in its
 // V is NaN.  In tiles with keys that some row does not see, rows past the
 // request's last key are zeroed in shared memory, and a non-finite V element
@@ -28,7 +34,9 @@
 // the epilogue gives rows that do see it the value the sum would have.
 //
 // Every wait on an mbarrier is bounded; on expiry the block records
-// PA_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and returns.
+// PA_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and returns.  No
+// barrier runs more than one phase ahead of a waiter: those that a role could
+// pass a whole piece early come in pairs, used in turn.
 #include <cudaTypedefs.h>
 
 #include "serving.h"
@@ -50,27 +58,38 @@ struct SvCfg {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = 2 * TILE_BYTES;
   static constexpr int OFF_V = OFF_K + 2 * TILE_BYTES;
-  static constexpr int OFF_BAR = OFF_V + 2 * TILE_BYTES;
-  static constexpr int SMEM_BYTES = OFF_BAR + 8192;
+  static constexpr int OFF_OUT = OFF_V + 2 * TILE_BYTES;   // output staging, 2 KB per softmax warp
+  static constexpr int OFF_BAR = OFF_OUT + 8 * 2048;
+  static constexpr int SMEM_BYTES = OFF_BAR + 13 * 1024;
   static constexpr float SCALE = static_cast<float>(kLog2e / (D == 128 ? 11.31370849898476039 : 8.0));  // log2(e) / sqrt(d)
   static constexpr uint32_t IDESC_QK = idesc_f16(128, 128, 1, 1, 0, 0);  // bf16 Q . bf16 K
   static constexpr uint32_t IDESC_PV = idesc_f16(128, D, 1, 1, 0, 1);    // bf16 P . bf16 V (MN-major)
 };
 
 struct SvBars {
-  uint64_t q_full;
+  uint64_t q_full, q_empty;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t vg_full[2];    // a guarded V tile has landed
   uint64_t v_ready[2];    // ... and has been checked
   uint64_t s_full[2], p_full[2], o_final[2];
+  uint64_t noted[2];      // the guard is through with a piece's tiles; pieces in turn
+  uint64_t done[2];       // the softmax warps have read a piece's O and notes; pieces in turn
+  uint64_t ml_full[2];    // a warpgroup's maxima and sums are written (one row tile)
+  uint64_t work_full[2];  // `work` holds a piece; pieces in turn
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  int nonfinite;          // some guarded V element was not finite
-  int first[3][128];      // per column: first key with +inf, -inf, NaN
-  float ml[2][2][128];    // one row tile: both warpgroups' maximum and sum per row
+  int odd[2];             // 1 + number of the piece that met a non-finite V
+  // per column: first key with +inf, -inf, NaN, below the complement of 1 + the
+  // piece's number, so that a later piece's entry is always the smaller
+  unsigned long long first[2][3][128];
+  float ml[2][2][2][128]; // [in turn][warpgroup][maximum, sum][row]
+  struct {
+    int4 piece[2];        // a Piece
+    int kvh;              // its kv head; -1: no more
+  } work[2];
 };
-static_assert(sizeof(SvBars) + 1024 <= 8192, "barriers and alignment slack");
+static_assert(sizeof(SvBars) + 1024 <= 13 * 1024, "barriers and alignment slack");
 
 struct SvParams {
   AttendArgs a;
@@ -90,14 +109,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-template <int ID, int N>
-__device__ __forceinline__ void bar_sync() {
-  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
-}
-template <int ID, int N>
-__device__ __forceinline__ void bar_arrive() {
-  asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(N) : "memory");
-}
 __device__ __forceinline__ bool bf16_nonfinite(uint32_t two) {
   return (two & 0x7f80u) == 0x7f80u || (two & 0x7f800000u) == 0x7f800000u;
 }
@@ -106,7 +117,7 @@ __device__ __forceinline__ bool bf16_nonfinite(uint32_t two) {
 // 128-byte swizzle): rows from `first_row` on may be masked, rows from
 // `n_keys` on hold no key.  Run by 64 threads.
 template <int D>
-__device__ void guard_tile(uint8_t* v, int first_row, int n_keys, int key0, SvBars* bars, int tid) {
+__device__ void guard_tile(uint8_t* v, int first_row, int n_keys, int key0, int piece, SvBars* bars, int tid) {
   using C = SvCfg<D>;
   constexpr int CH = D / 8;   // 16-byte chunks of a row
   for (int i = first_row * CH + tid; i < 128 * CH; i += 64) {
@@ -122,13 +133,47 @@ __device__ void guard_tile(uint8_t* v, int first_row, int n_keys, int key0, SvBa
       for (int k = 0; k < 8; ++k)
         if ((e[k] & 0x7f80) == 0x7f80) {
           const int kind = (e[k] & 0x7f) ? 2 : (e[k] >> 15);
-          atomicMin(&bars->first[kind][8 * c + k], key0 + r);
+          atomicMin(&bars->first[piece & 1][kind][8 * c + k],
+                    (static_cast<unsigned long long>(~static_cast<uint32_t>(piece + 1)) << 32) | static_cast<uint32_t>(key0 + r));
           e[k] = 0;
         }
       *p = x;
-      bars->nonfinite = 1;
+      bars->odd[piece & 1] = piece + 1;
     }
   }
+}
+
+// A piece as its roles see it.
+struct Item {
+  Piece pc;
+  int kvh;
+  int ctx;        // position of the first new token (may be negative)
+  int n;          // key tiles
+  bool two;       // two row tiles
+  int nt0, nt1;   // key tiles of each warpgroup: with two row tiles those up to its
+                  // last row's limit, of all; with one, every other
+  int g0;         // first guarded tile: tiles from it on hold a key that the first row does not see
+};
+
+// The k-th piece of this block, once it is there; false: no more.
+__device__ __forceinline__ bool get_item(const SvBars* bars, int tpt, int k, Item& it) {
+  const int4 x = bars->work[k & 1].piece[0], y = bars->work[k & 1].piece[1];
+  it.kvh = bars->work[k & 1].kvh;
+  it.pc = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  const Piece& pc = it.pc;
+  it.ctx = pc.kv_len - pc.q_len;
+  it.n = pc.kt1 - pc.kt0;
+  it.two = pc.tok0 + tpt < pc.q_len;
+  if (it.two) {
+    const int seen = max(0, it.ctx + pc.tok0 + tpt);    // keys that tile 0 sees (it is full)
+    it.nt0 = max(0, min(it.n, (seen + kKeyTile - 1) / kKeyTile - pc.kt0));
+    it.nt1 = it.n;
+  } else {
+    it.nt0 = (it.n + 1) / 2;
+    it.nt1 = it.n / 2;
+  }
+  it.g0 = max(0, max(0, it.ctx + pc.tok0 + 1) / kKeyTile - pc.kt0);
+  return it.kvh >= 0;
 }
 
 template <int D, bool PAGED>
@@ -148,6 +193,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_empty[s], 1);
@@ -158,13 +204,17 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->p_full[s], 128);
       mbar_init(&bars->o_final[s], 1);
+      mbar_init(&bars->noted[s], 64);
+      mbar_init(&bars->done[s], 256);
+      mbar_init(&bars->ml_full[s], 128);
+      mbar_init(&bars->work_full[s], 1);
+      bars->odd[s] = 0;
     }
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
-    bars->nonfinite = 0;
     fence_mbar_init();
   }
-  for (int i = threadIdx.x; i < 3 * 128; i += 384) bars->first[0][i] = INT32_MAX;
+  for (int i = threadIdx.x; i < 2 * 3 * 128; i += 384) (&bars->first[0][0][0])[i] = ~0ull;
   if (warp == 2) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
@@ -177,105 +227,121 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars->tmem_base;
   grid_dep_wait();      // the set-up above overlaps the plan
   grid_dep_launch();
-  int at, kvh;
-  if (!piece_of_block(a, &at, &kvh)) {
-    if (warp == 2) tmem_dealloc(tmem, 512);
-    return;
-  }
-  const Piece pc = a.pieces[at];
+  const uint32_t tmem = bars->tmem_base;
   volatile int* abort = &bars->abort;
   volatile int* gabort = &a.head->abort;
   const int g = a.hq / a.hkv;
   const int tpt = 128 / g;                           // tokens per row tile
-  const int ctx = pc.kv_len - pc.q_len;              // position of the first new token (may be negative)
-  const int n = pc.kt1 - pc.kt0;                     // key tiles of this piece
-  const bool two = pc.tok0 + tpt < pc.q_len;         // two row tiles
-  // key tiles of warpgroup t: with two row tiles those up to its last row's
-  // limit, of all; with one, every other
-  int nt[2];
-  if (two) {
-    const int seen = max(0, ctx + pc.tok0 + tpt);    // keys that tile 0 sees (it is full)
-    nt[0] = max(0, min(n, (seen + kKeyTile - 1) / kKeyTile - pc.kt0));
-    nt[1] = n;
-  } else {
-    nt[0] = (n + 1) / 2;
-    nt[1] = n / 2;
-  }
-  // tiles from jg on hold a key that the piece's first row does not see
-  const int jg = max(0, ctx + pc.tok0 + 1) / kKeyTile;
-  const int g0 = max(0, jg - pc.kt0);                // first guarded tile of this piece
   auto fail = [&](int where) {
     *abort = 1;
     *gabort = 1;
     set_status(a.status, PA_ERR_TIMEOUT, static_cast<int>(blockIdx.x), where);
   };
-  auto wait_one = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort, a.wait_limit_ns, gabort); };
+  auto wait_one = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait(bar, parity & 1, abort, a.wait_limit_ns, gabort);
+  };
   // the same for a whole warp, one answer for all lanes
   auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const int nbox = kKeyTile / p.box_rows;
-    // row coordinate of this lane's box of tile j
-    auto row_of = [&](int j) -> int {
-      if (!PAGED) return pc.row0 + j * kKeyTile;
-      const int64_t key = static_cast<int64_t>(j) * kKeyTile + lane * p.box_rows;
-      if (lane >= nbox || key >= pc.kv_len) return p.oob_row;
-      const int64_t slot = key_slot(a, pc.b, key);
-      return slot < 0 ? p.oob_row : static_cast<int>(slot);
+    const int q_bytes = tpt * g * 128 * C::NKB;
+    uint32_t tile = 0;                  // K and V tiles before this one
+    uint32_t n_q = 0, n_k = 0;          // copies issued: Q's and K tiles,
+    uint32_t n_v0 = 0, n_v1 = 0, n_g0 = 0, n_g1 = 0;   // V tiles of each stage, guarded ones
+    // Units of work: this block's first, then whichever comes next over all
+    // blocks (the deepest come first, so the blocks end together).  Lane l of
+    // the first two holds the l-th half of the piece after the current one.
+    const unsigned total = static_cast<unsigned>(a.head->n_pieces) * static_cast<unsigned>(a.hkv);
+    unsigned unit = blockIdx.x;
+    int at = 0, kvh = -1;
+    int4 half = make_int4(0, 0, 0, 0);
+    auto fetch = [&]() {
+      kvh = -1;
+      if (unit < total) {
+        piece_at(a, unit, &at, &kvh);
+        if (lane < 2) half = reinterpret_cast<const int4*>(a.pieces + at)[lane];
+      }
     };
-    int row = n > 0 ? row_of(pc.kt0) : 0;
-    if (lane == 0) {
-      const int qt = two ? 2 : 1;
-      const int q_bytes = tpt * g * 128 * C::NKB;
-      mbar_arrive_expect_tx(&bars->q_full, qt * q_bytes);
-      for (int t = 0; t < qt; ++t)
-        for (int kb = 0; kb < C::NKB; ++kb)
-          tma_load_3d(sQ + t * C::TILE_BYTES + kb * C::KB_BYTES, &tmQ, &bars->q_full, kb * 64, kvh * g,
-                      pc.row0 + pc.tok0 + t * tpt);
-    }
-    int n_k = 0, n_v = 0;   // K and V tiles issued
-    for (int jj = 0; jj < n; ++jj) {
-      const int st = jj & 1;
-      const uint32_t ph = (jj >> 1) & 1;
-      const int next = jj + 1 < n ? row_of(pc.kt0 + jj + 1) : 0;
-      if (!wait(&bars->k_empty[st], ph ^ 1)) break;
-      if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], C::TILE_BYTES);
+    fetch();
+    bool ok = true;
+    Item it;
+    for (int k = 0; ok; ++k) {
+      // the slot's previous piece (two before) is finished
+      if (k >= 2 && !wait(&bars->done[k & 1], (k >> 1) - 1)) { ok = false; break; }
+      if (lane < 2) bars->work[k & 1].piece[lane] = half;
+      if (lane == 2) bars->work[k & 1].kvh = kvh;
       __syncwarp();
-      if (lane < nbox)
-        for (int kb = 0; kb < C::NKB; ++kb)
-          tma_load_3d(sK + st * C::TILE_BYTES + kb * C::KB_BYTES + lane * p.box_rows * 128, &tmK, &bars->k_full[st],
-                      kb * 64, kvh, row);
-      ++n_k;
-      if (!wait(&bars->v_empty[st], ph ^ 1)) break;
-      uint64_t* full = jj >= g0 ? &bars->vg_full[st] : &bars->v_full[st];
-      if (lane == 0) mbar_arrive_expect_tx(full, C::TILE_BYTES);
-      __syncwarp();
-      if (lane < nbox)
-        for (int kb = 0; kb < C::NKB; ++kb)
-          tma_load_3d(sV + st * C::TILE_BYTES + kb * C::KB_BYTES + lane * p.box_rows * 128, &tmV, full, kb * 64,
-                      kvh, row);
-      ++n_v;
-      row = next;
+      if (lane == 0) mbar_arrive(&bars->work_full[k & 1]);
+      if (!get_item(bars, tpt, k, it)) break;
+      if (lane == 0) unit = gridDim.x + atomicAdd(&a.head->next, 1u);
+      unit = __shfl_sync(0xffffffffu, unit, 0);
+      fetch();
+      const Piece& pc = it.pc;
+      // row coordinate of this lane's box of tile j
+      auto row_of = [&](int j) -> int {
+        if (!PAGED) return pc.row0 + j * kKeyTile;
+        const int64_t key = static_cast<int64_t>(j) * kKeyTile + lane * p.box_rows;
+        if (lane >= nbox || key >= pc.kv_len) return p.oob_row;
+        const int64_t slot = key_slot(a, pc.b, key);
+        return slot < 0 ? p.oob_row : static_cast<int>(slot);
+      };
+      int row = it.n > 0 ? row_of(pc.kt0) : 0;
+      if (k > 0 && !wait(&bars->q_empty, k - 1)) { ok = false; break; }
+      if (lane == 0) {
+        const int qt = it.two ? 2 : 1;
+        mbar_arrive_expect_tx(&bars->q_full, qt * q_bytes);
+        for (int t = 0; t < qt; ++t)
+          for (int kb = 0; kb < C::NKB; ++kb)
+            tma_load_3d(sQ + t * C::TILE_BYTES + kb * C::KB_BYTES, &tmQ, &bars->q_full, kb * 64, it.kvh * g,
+                        pc.row0 + pc.tok0 + t * tpt);
+      }
+      ++n_q;
+      for (int jj = 0; jj < it.n; ++jj, ++tile) {
+        const int st = tile & 1;
+        const uint32_t ph = tile >> 1;
+        const int next = jj + 1 < it.n ? row_of(pc.kt0 + jj + 1) : 0;
+        if (!wait(&bars->k_empty[st], ph + 1)) { ok = false; break; }
+        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], C::TILE_BYTES);
+        __syncwarp();
+        if (lane < nbox)
+          for (int kb = 0; kb < C::NKB; ++kb)
+            tma_load_3d(sK + st * C::TILE_BYTES + kb * C::KB_BYTES + lane * p.box_rows * 128, &tmK,
+                        &bars->k_full[st], kb * 64, it.kvh, row);
+        ++n_k;
+        if (!wait(&bars->v_empty[st], ph + 1)) { ok = false; break; }
+        const bool guarded = jj >= it.g0;
+        uint64_t* full = guarded ? &bars->vg_full[st] : &bars->v_full[st];
+        if (lane == 0) mbar_arrive_expect_tx(full, C::TILE_BYTES);
+        __syncwarp();
+        if (lane < nbox)
+          for (int kb = 0; kb < C::NKB; ++kb)
+            tma_load_3d(sV + st * C::TILE_BYTES + kb * C::KB_BYTES + lane * p.box_rows * 128, &tmV, full, kb * 64,
+                        it.kvh, row);
+        n_v0 += !guarded && st == 0;
+        n_v1 += !guarded && st == 1;
+        n_g0 += guarded && st == 0;
+        n_g1 += guarded && st == 1;
+        row = next;
+      }
     }
     if (lane == 0) {
-      if (n_v < n) fail(1);
+      if (!ok) fail(1);
       // Drain: every copy this warp started has landed before the block ends.
       int zero = 0;
-      mbar_wait(&bars->q_full, 0, &zero, a.wait_limit_ns);
-      for (int s = 0; s < 2; ++s) {
-        const int uk = (n_k + 1 - s) >> 1;                             // K tiles of stage s
-        if (uk > 0) mbar_wait(&bars->k_full[s], (uk - 1) & 1, &zero, a.wait_limit_ns);
-        const int nu = min(n_v, g0);                                   // unguarded V tiles
-        const int uv = (nu + 1 - s) >> 1;
-        if (uv > 0) mbar_wait(&bars->v_full[s], (uv - 1) & 1, &zero, a.wait_limit_ns);
-        const int ng = n_v - nu;                                       // guarded ones, from tile g0 on
-        const int ug = (ng + 1 - ((s ^ g0) & 1)) >> 1;
-        if (ug > 0) mbar_wait(&bars->vg_full[s], (ug - 1) & 1, &zero, a.wait_limit_ns);
-      }
+      auto landed = [&](uint64_t* bar, uint32_t count) {
+        if (count > 0) mbar_wait(bar, (count - 1) & 1, &zero, a.wait_limit_ns);
+      };
+      landed(&bars->q_full, n_q);
+      landed(&bars->k_full[0], (n_k + 1) >> 1);
+      landed(&bars->k_full[1], n_k >> 1);
+      landed(&bars->v_full[0], n_v0);
+      landed(&bars->v_full[1], n_v1);
+      landed(&bars->vg_full[0], n_g0);
+      landed(&bars->vg_full[1], n_g1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
@@ -283,9 +349,10 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(sV), C::KB_BYTES, 1024);
-      auto qk = [&](int t, int st) {
+      // scores of warpgroup t from row tile qt
+      auto qk = [&](int t, int qt, int st) {
         const uint32_t d_tmem = tmem + t * 256;
-        const uint64_t qd = sdesc_add(q_desc, two ? t * C::TILE_BYTES : 0);
+        const uint64_t qd = sdesc_add(q_desc, qt * C::TILE_BYTES);
         const uint64_t kd = sdesc_add(k_desc, st * C::TILE_BYTES);
 #pragma unroll
         for (int kb = 0; kb < C::NKB; ++kb)
@@ -293,6 +360,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
           for (int ks = 0; ks < 4; ++ks)
             mma_ss(d_tmem, sdesc_add(qd, kb * C::KB_BYTES + ks * 32), sdesc_add(kd, kb * C::KB_BYTES + ks * 32),
                    C::IDESC_QK, (kb | ks) != 0);
+        mma_commit(&bars->s_full[t]);
       };
       auto pv = [&](int t, int st, int acc) {
         const uint32_t d_tmem = tmem + t * 256 + 128;
@@ -301,65 +369,86 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
         for (int ks = 0; ks < 8; ++ks)
           mma_ts(d_tmem, tmem + t * 256 + ks * 8, sdesc_add(vd, ks * 2048), C::IDESC_PV, (acc | ks) != 0);
       };
-      auto wait_k = [&](int jj) { return wait_one(&bars->k_full[jj & 1], (jj >> 1) & 1); };
-      auto wait_v = [&](int jj) {
-        return jj < g0 ? wait_one(&bars->v_full[jj & 1], (jj >> 1) & 1) : wait_one(&bars->v_ready[jj & 1], ((jj - g0) >> 1) & 1);
+      uint32_t tile = 0;                        // K and V tiles before this piece
+      // phases, one bit each: of each warpgroup's P, and of each stage's V
+      // tiles and guarded V tiles
+      uint32_t ph_p = 0, ph_v = 0, ph_g = 0;
+      auto next = [](uint32_t& bits, int i) {
+        const uint32_t b = (bits >> i) & 1;
+        bits ^= 1u << i;
+        return b;
       };
-      bool ok = wait_one(&bars->q_full, 0);
-      if (!ok) fail(3);
-      if (two) {
-        for (int jj = 0; ok && jj < n; ++jj) {
-          const int st = jj & 1, st1 = st ^ 1;
-          if (jj == 0) {
-            if (!wait_k(0)) { fail(4); break; }
-            tc_fence_after();
-            for (int t = 0; t < 2; ++t)
-              if (nt[t] > 0) {
-                qk(t, 0);
-                mma_commit(&bars->s_full[t]);
+      auto wait_k = [&](uint32_t x) { return wait_one(&bars->k_full[x & 1], x >> 1); };
+      bool ok = true;
+      Item it;
+      for (int k = 0; ok; ++k, tile += it.n) {
+        if (!wait_one(&bars->work_full[k & 1], k >> 1)) { fail(2); break; }
+        if (!get_item(bars, tpt, k, it)) break;
+        const int n = it.n;
+        auto wait_v = [&](int jj) {
+          const int st = (tile + jj) & 1;
+          return jj < it.g0 ? wait_one(&bars->v_full[st], next(ph_v, st)) : wait_one(&bars->v_ready[st], next(ph_g, st));
+        };
+        // the previous piece's O has been read before the first P V of this one
+        auto wait_o = [&]() { return k == 0 || wait_one(&bars->done[(k - 1) & 1], (k - 1) >> 1); };
+        if (!wait_one(&bars->q_full, k)) { fail(3); break; }
+        if (n == 0) {
+          mma_commit(&bars->q_empty);
+        } else if (it.two) {
+          if (!wait_k(tile)) { fail(4); break; }
+          tc_fence_after();
+          if (it.nt0 > 0) qk(0, 0, tile & 1);
+          qk(1, 1, tile & 1);
+          mma_commit(&bars->k_empty[tile & 1]);
+          if (n == 1) mma_commit(&bars->q_empty);
+          for (int jj = 0; ok && jj < n; ++jj) {
+            const int st = (tile + jj) & 1, st1 = st ^ 1;
+            // V_j and K_{j+1} first, while the tensor pipe still runs the other
+            // tile's MMAs, so that nothing stands between P and its products
+            if (!wait_v(jj)) { fail(6); ok = false; break; }
+            if (jj + 1 < n && !wait_k(tile + jj + 1)) { fail(7); ok = false; break; }
+            if (jj == 0 && !wait_o()) { fail(12); ok = false; break; }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int nt = t == 0 ? it.nt0 : n;
+              if (jj < nt) {
+                if (!wait_one(&bars->p_full[t], next(ph_p, t))) { fail(5); ok = false; break; }
+                tc_fence_after();
+                pv(t, st, jj > 0);
+                if (jj == nt - 1) mma_commit(&bars->o_final[t]);
               }
-            mma_commit(&bars->k_empty[0]);
-          }
-          // V_j and K_{j+1} first, while the tensor pipe still runs the other
-          // tile's MMAs, so that nothing stands between P and its products
-          if (!wait_v(jj)) { fail(6); break; }
-          if (jj + 1 < n && !wait_k(jj + 1)) { fail(7); break; }
-          for (int t = 0; t < 2; ++t) {
-            if (jj < nt[t]) {
-              if (!wait_one(&bars->p_full[t], jj & 1)) { fail(5); ok = false; break; }
-              tc_fence_after();
-              pv(t, st, jj > 0);
-              if (jj == nt[t] - 1) mma_commit(&bars->o_final[t]);
+              if (t == 1) mma_commit(&bars->v_empty[st]);
+              if (jj + 1 < nt) qk(t, t, st1);
             }
-            if (t == 1) mma_commit(&bars->v_empty[st]);
-            if (jj + 1 < nt[t]) {
-              qk(t, st1);
-              mma_commit(&bars->s_full[t]);
+            if (ok && jj + 1 < n) {
+              mma_commit(&bars->k_empty[st1]);
+              if (jj + 2 == n) mma_commit(&bars->q_empty);
             }
           }
-          if (ok && jj + 1 < n) mma_commit(&bars->k_empty[st1]);
-        }
-      } else if (ok && n > 0) {
-        for (int jj = 0; jj < min(n, 2); ++jj) {
-          if (!wait_k(jj)) { fail(4); ok = false; break; }
-          tc_fence_after();
-          qk(jj, jj);
-          mma_commit(&bars->s_full[jj]);
-          mma_commit(&bars->k_empty[jj]);
-        }
-        for (int jj = 0; ok && jj < n; ++jj) {
-          const int t = jj & 1, i = jj >> 1;
-          if (!wait_v(jj)) { fail(6); break; }
-          if (jj + 2 < n && !wait_k(jj + 2)) { fail(7); break; }
-          if (!wait_one(&bars->p_full[t], i & 1)) { fail(5); break; }
-          tc_fence_after();
-          pv(t, t, i > 0);
-          if (i == nt[t] - 1) mma_commit(&bars->o_final[t]);
-          mma_commit(&bars->v_empty[t]);
-          if (jj + 2 < n) {
-            qk(t, t);
-            mma_commit(&bars->s_full[t]);
-            mma_commit(&bars->k_empty[t]);
+        } else {
+          for (int jj = 0; jj < min(n, 2); ++jj) {
+            if (!wait_k(tile + jj)) { fail(4); ok = false; break; }
+            tc_fence_after();
+            qk(jj, 0, (tile + jj) & 1);
+            mma_commit(&bars->k_empty[(tile + jj) & 1]);
+          }
+          if (!ok) break;
+          if (n <= 2) mma_commit(&bars->q_empty);
+          for (int jj = 0; jj < n; ++jj) {
+            const int t = jj & 1, i = jj >> 1, st = (tile + jj) & 1;
+            if (!wait_v(jj)) { fail(6); ok = false; break; }
+            if (jj + 2 < n && !wait_k(tile + jj + 2)) { fail(7); ok = false; break; }
+            if (jj == 0 && !wait_o()) { fail(12); ok = false; break; }
+            if (!wait_one(&bars->p_full[t], next(ph_p, t))) { fail(5); ok = false; break; }
+            tc_fence_after();
+            pv(t, st, i > 0);
+            if (jj + 2 >= n) mma_commit(&bars->o_final[t]);
+            mma_commit(&bars->v_empty[st]);
+            if (jj + 2 < n) {
+              qk(t, 0, st);
+              mma_commit(&bars->k_empty[st]);
+              if (jj + 3 == n) mma_commit(&bars->q_empty);
+            }
           }
         }
       }
@@ -371,229 +460,239 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
   } else if (warp < 4) {
     // ---------------------------------------------------------- V guard
     const int tid = threadIdx.x - 64;
-    const int lim_first = ctx + pc.tok0;
-    for (int jj = g0; jj < n; ++jj) {
-      const int st = jj & 1, i = (jj - g0) >> 1;
-      if (!wait(&bars->vg_full[st], i & 1)) { if (lane == 0) fail(11); break; }
-      const int key0 = (pc.kt0 + jj) * kKeyTile;
-      guard_tile<D>(sV + st * C::TILE_BYTES, max(0, lim_first + 1 - key0), pc.kv_len - key0, key0, bars, tid);
-      fence_async_smem();
-      mbar_arrive(&bars->v_ready[st]);
+    uint32_t tile = 0, ph_g = 0;   // ph_g: phase bit of each stage's guarded tiles
+    bool ok = true;
+    Item it;
+    for (int k = 0; ok; ++k, tile += it.n) {
+      // (a piece is there only when the one two before, whose notes it takes over, is finished)
+      if (!wait(&bars->work_full[k & 1], k >> 1)) { ok = false; break; }
+      if (!get_item(bars, tpt, k, it)) break;
+      const int lim_first = it.ctx + it.pc.tok0;
+      for (int jj = it.g0; jj < it.n; ++jj) {
+        const int st = (tile + jj) & 1;
+        if (!wait(&bars->vg_full[st], ph_g >> st)) { ok = false; break; }
+        ph_g ^= 1u << st;
+        const int key0 = (it.pc.kt0 + jj) * kKeyTile;
+        guard_tile<D>(sV + st * C::TILE_BYTES, max(0, lim_first + 1 - key0), it.pc.kv_len - key0, key0, k, bars, tid);
+        fence_async_smem();
+        mbar_arrive(&bars->v_ready[st]);
+      }
+      mbar_arrive(&bars->noted[k & 1]);
     }
-    bar_arrive<1, 192>();   // one barrier per softmax warpgroup: neither waits for the other here
-    bar_arrive<2, 192>();
+    if (!ok && lane == 0) fail(11);
   } else {
     // -------------------------------------------------------------- softmax
     const int t = warp >= 8 ? 1 : 0;
     const int sub = warp & 3;
     const int rl = sub * 32 + lane;
-    const int tok_t = pc.tok0 + (two ? t * tpt : 0);     // first token of this warpgroup's rows
-    const int tok = tok_t + rl / g;
-    const bool valid = rl < tpt * g && tok < pc.q_len;
-    const int lim = valid ? ctx + tok : pc.kv_len - 1;   // last visible key
-    const int lim_w = ctx + tok_t + sub * 32 / g;        // the smallest of this warp's rows
+    const uint32_t ginv = 65536u / g + 1;            // row / g for rows below 128, g <= 64: exact
+    const int rt = static_cast<int>((rl * ginv) >> 16), rh = rl - rt * g;   // token and head of this thread's row
     const uint32_t s_tmem = tmem + (static_cast<uint32_t>(sub * 32) << 16) + t * 256;
     const uint32_t o_tmem = s_tmem + 128;
-    const int my = nt[t];
+    const uint32_t o_oth = tmem + (static_cast<uint32_t>(sub * 32) << 16) + (t ^ 1) * 256 + 128;
     const uint64_t sc2 = f2_pack(C::SCALE, C::SCALE);
-    float m_run = -INFINITY, l_run = 0.f;
+    uint8_t* stage = smem + C::OFF_OUT + (warp - 4) * 2048;
+    uint32_t n_s = 0, n_own = 0, n_oth = 0, n_ml = 0;   // phases: scores, both final O's, exchanged maxima
     bool ok = true;
-    for (int i = 0; i < my; ++i) {
-      const int key0 = (pc.kt0 + (two ? i : 2 * i + t)) * kKeyTile;
-      if (!wait(&bars->s_full[t], i & 1)) { fail(9); ok = false; break; }
-      tc_fence_after();
-      uint32_t sr[128];
-      tmem_ld_x128(s_tmem, sr);
-      if (key0 + kKeyTile - 1 > lim_w) {
-        const int rel = lim - key0;                      // columns <= rel are visible
-#pragma unroll
-        for (int e = 0; e < 128; ++e)
-          if (e > rel) sr[e] = __float_as_uint(-INFINITY);
+    for (int k = 0; ok; ++k) {
+      // (read again for the output, so that little of it is held in registers beside the scores)
+      int my, lim, lim_w, key_first, key_step;
+      {
+        if (!wait(&bars->work_full[k & 1], k >> 1)) { ok = false; break; }
+        Item it;
+        if (!get_item(bars, tpt, k, it)) break;
+        const int tok_t = it.pc.tok0 + (it.two ? t * tpt : 0);   // first token of this warpgroup's rows
+        const bool valid = rl < tpt * g && tok_t + rt < it.pc.q_len;
+        lim = valid ? it.ctx + tok_t + rt : it.pc.kv_len - 1;                         // last visible key
+        lim_w = it.ctx + tok_t + static_cast<int>((sub * 32 * ginv) >> 16);           // the smallest of this warp's rows
+        my = t == 0 ? it.nt0 : it.nt1;
+        key_first = (it.pc.kt0 + (it.two ? 0 : t)) * kKeyTile;
+        key_step = it.two ? kKeyTile : 2 * kKeyTile;
       }
-      float mx[8];
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int i = 0; i < my; ++i) {
+        const int key0 = key_first + i * key_step;
+        if (!wait(&bars->s_full[t], n_s++)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t sr[128];
+        tmem_ld_x128(s_tmem, sr);
+        if (key0 + kKeyTile - 1 > lim_w) {
+          const int rel = lim - key0;                      // columns <= rel are visible
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mx[e] = -INFINITY;
-#pragma unroll
-      for (int e = 0; e < 64; ++e)
-        mx[e & 7] = fmax3(mx[e & 7], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
-      const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
-      const float m_new = fmaxf(m_run, mt);
-      const bool need = (m_new - m_run) * C::SCALE > 8.f;   // lazy rescale: only when P could exceed 2^8
-      float alpha = 1.f;
-      if (need) {
-        alpha = fast_exp2((m_run - m_new) * C::SCALE);
-        m_run = m_new;
-      }
-      const float m_use = (m_run == -INFINITY) ? 0.f : m_run * C::SCALE;
-      const uint64_t nm2 = f2_pack(-m_use, -m_use);
-      uint64_t acc2[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc2[e] = 0ull;   // two 0.0f
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float x0, x1, p0, p1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])),
-                           sc2, nm2), x0, x1);
-          p0 = fast_exp2(x0);
-          p1 = fast_exp2(x1);
-          acc2[e & 3] = f2_add(acc2[e & 3], f2_pack(p0, p1));
-          pk[e] = pack2(p0, p1);
+          for (int e = 0; e < 128; ++e)
+            if (e > rel) sr[e] = __float_as_uint(-INFINITY);
         }
-        tmem_st_x16(s_tmem + 16 * c, pk);
-      }
-      float sum = 0.f;
+        float mx[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float a0, a1;
-        f2_unpack(acc2[e], a0, a1);
-        sum += a0 + a1;
-      }
-      l_run = l_run * alpha + sum;
-      if (i > 0 && __any_sync(0xffffffffu, need)) {
-        // O was last written by the previous PV, which completed before this
-        // S (the commit signalling S covers every earlier MMA).
+        for (int e = 0; e < 8; ++e) mx[e] = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t ov[32];
-          tmem_ld_x32(o_tmem + 32 * c, ov);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-          tmem_st_x32(o_tmem + 32 * c, ov);
+        for (int e = 0; e < 64; ++e)
+          mx[e & 7] = fmax3(mx[e & 7], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+        const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
+        const float m_new = fmaxf(m_run, mt);
+        const bool need = (m_new - m_run) * C::SCALE > 8.f;   // lazy rescale: only when P could exceed 2^8
+        float alpha = 1.f;
+        if (need) {
+          alpha = fast_exp2((m_run - m_new) * C::SCALE);
+          m_run = m_new;
         }
+        const float m_use = (m_run == -INFINITY) ? 0.f : m_run * C::SCALE;
+        const uint64_t nm2 = f2_pack(-m_use, -m_use);
+        uint64_t acc2[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc2[e] = 0ull;   // two 0.0f
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1, p0, p1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])),
+                             sc2, nm2), x0, x1);
+            p0 = fast_exp2(x0);
+            p1 = fast_exp2(x1);
+            acc2[e & 3] = f2_add(acc2[e & 3], f2_pack(p0, p1));
+            pk[e] = pack2(p0, p1);
+          }
+          tmem_st_x16(s_tmem + 16 * c, pk);
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float a0, a1;
+          f2_unpack(acc2[e], a0, a1);
+          sum += a0 + a1;
+        }
+        l_run = l_run * alpha + sum;
+        if (i > 0 && __any_sync(0xffffffffu, need)) {
+          // O was last written by the previous PV, which completed before this
+          // S (the commit signalling S covers every earlier MMA).
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tmem_ld_x32(o_tmem + 32 * c, ov);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+            tmem_st_x32(o_tmem + 32 * c, ov);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[t]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&bars->p_full[t]);
-    }
-    if (t == 0) bar_sync<1, 192>();   // the guard's notes are complete
-    else bar_sync<2, 192>();
-    // Rows' final maximum and sum.  Weights w0, w1 of the two O's (one row
-    // tile) or w0 of its own (two).
-    const int n_other = nt[t ^ 1];
-    if (ok && (my > 0 || (!two && n_other > 0))) {
-      if (my > 0 && !wait(&bars->o_final[t], 0)) { fail(10); ok = false; }
-      if (ok && !two && n_other > 0 && !wait(&bars->o_final[t ^ 1], 0)) { fail(10); ok = false; }
-    } else if (ok) {
-      // no key tile: nothing was computed, but Q's copy may still be landing
-      // in the memory that stages the output
-      if (!wait(&bars->q_full, 0)) { fail(10); ok = false; }
-    }
-    float w_own = 1.f, w_oth = 0.f;
-    if (!two) {
-      bars->ml[t][0][rl] = m_run;
-      bars->ml[t][1][rl] = l_run;
-      bar_sync<3, 256>();
-      const float m2 = bars->ml[t ^ 1][0][rl], l2 = bars->ml[t ^ 1][1][rl];
-      const float m = fmaxf(m_run, m2);
-      if (m != -INFINITY) {
-        w_own = fast_exp2((m_run - m) * C::SCALE);
-        w_oth = fast_exp2((m2 - m) * C::SCALE);
+      if (!ok) break;
+      // ---- the piece's output: its own O (two row tiles), or half of the
+      // columns of both O's joined (one)
+      if (!wait(&bars->noted[k & 1], k >> 1)) { ok = false; break; }
+      Item it;
+      get_item(bars, tpt, k, it);
+      const Piece& pc = it.pc;
+      const bool two = it.two;
+      const int tok_t = pc.tok0 + (two ? t * tpt : 0);
+      const bool valid = rl < tpt * g && tok_t + rt < pc.q_len;
+      const int n_other = t == 0 ? it.nt1 : it.nt0;
+      float w_own = 1.f, w_oth = 0.f;
+      if (!two) {
+        float (*ml)[2][128] = bars->ml[n_ml & 1];
+        ml[t][0][rl] = m_run;
+        ml[t][1][rl] = l_run;
+        mbar_arrive(&bars->ml_full[t]);
+        if (!wait(&bars->ml_full[t ^ 1], n_ml++)) { ok = false; break; }
+        const float m2 = ml[t ^ 1][0][rl], l2 = ml[t ^ 1][1][rl];
+        const float m = fmaxf(m_run, m2);
+        if (m != -INFINITY) {
+          w_own = fast_exp2((m_run - m) * C::SCALE);
+          w_oth = fast_exp2((m2 - m) * C::SCALE);
+        }
+        l_run = l_run * w_own + l2 * w_oth;
+        m_run = m;
       }
-      l_run = l_run * w_own + l2 * w_oth;
-      m_run = m;
-    }
-    if (ok) {
+      if (my > 0 && !wait(&bars->o_final[t], n_own)) { ok = false; break; }
+      if (!two && n_other > 0 && !wait(&bars->o_final[t ^ 1], n_oth)) { ok = false; break; }
+      n_own += my > 0;
+      n_oth += n_other > 0;
       tc_fence_after();
       const bool empty = l_run == 0.f;               // no visible key (a NaN sum is not zero)
       const float inv = empty ? 0.f : 1.f / l_run;
       const float lse = empty ? -INFINITY : ((m_run == -INFINITY ? 0.f : m_run * C::SCALE) + log2f(l_run)) * kLn2f;
       w_own *= inv;
       w_oth *= inv;
-      const bool odd = *reinterpret_cast<volatile int*>(&bars->nonfinite) != 0;
-      // with one row tile each warpgroup writes half of the columns
-      constexpr int CHUNKS = D / 32;
-      const int c0 = two ? 0 : t * (CHUNKS / 2), nc = two ? CHUNKS : CHUNKS / 2;
-      const uint32_t o_oth = tmem + (static_cast<uint32_t>(sub * 32) << 16) + (t ^ 1) * 256 + 128;
-      // staging of this warp's rows for whole-row stores, in Q's memory
-      // (every QK^T has been read by now)
-      uint8_t* stage = sQ + (warp - 4) * 32 * D * 2;
-      const int64_t prow = (static_cast<int64_t>(pc.part) * a.hkv + kvh) * a.tile_rows + (two ? t * tpt * g : 0) + rl;
-      // columns 32 c .. 32 c + 31 of this thread's row
-      auto emit = [&](int c, float (&v)[32]) {
-        if (odd) {
-          for (int e = 0; e < 32; ++e) {
-            const int col = 32 * c + e;
-            const bool pos = bars->first[0][col] <= lim, neg = bars->first[1][col] <= lim;
-            float add = 0.f;
-            if (bars->first[2][col] <= lim || (pos && neg)) add = __int_as_float(0x7fc00000);
-            else if (pos) add = INFINITY;
-            else if (neg) add = -INFINITY;
+      const bool odd = *reinterpret_cast<volatile int*>(&bars->odd[k & 1]) == k + 1;
+      const int64_t prow = (static_cast<int64_t>(pc.part) * a.hkv + it.kvh) * a.tile_rows + (two ? t * tpt * g : 0) + rl;
+      const int rows = min(tpt, pc.q_len - tok_t) * g;     // rows of this tile
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) +
+                           ((static_cast<int64_t>(pc.row0) + tok_t) * a.hq + it.kvh * g) * D;
+      if (valid && (two || t == 0)) {
+        if (pc.part >= 0) a.part_lse[prow] = lse;
+        else if (a.lse) a.lse[(static_cast<int64_t>(pc.row0) + tok_t + rt) * a.hq + it.kvh * g + rh] = lse;
+      }
+      // 32 columns at a time; with one row tile each warpgroup writes half of them
+      const int c_lo = two ? 0 : t * (D / 2), c_hi = two ? D : c_lo + D / 2;
+#pragma unroll 1
+      for (int c = c_lo; c < c_hi; c += 32) {
+        uint32_t ov[32];
+        float v[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (k == e) v[k] += add;
-          }
+        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        if (my > 0) {
+          tmem_ld_x32(o_tmem + c, ov);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = empty ? 0.f : __uint_as_float(ov[e]) * w_own;
+        }
+        if (!two && n_other > 0) {
+          tmem_ld_x32(o_oth + c, ov);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] += empty ? 0.f : __uint_as_float(ov[e]) * w_oth;
         }
         if (pc.part >= 0) {
           if (valid) {
-            float4* d4 = reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c);
+            float4* d4 = reinterpret_cast<float4*>(a.part_o + prow * D + c);
 #pragma unroll
             for (int e = 0; e < 8; ++e) d4[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
           }
         } else {
+          // through shared memory, so that a store writes 64-byte pieces of rows
+          __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int ch = 4 * c + e;     // 16-byte chunk of the row, spread over the banks by row
-            *reinterpret_cast<uint4*>(stage + lane * D * 2 + ((ch ^ (lane & 7)) << 4)) =
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
                 make_uint4(pack2(v[8 * e], v[8 * e + 1]), pack2(v[8 * e + 2], v[8 * e + 3]),
                            pack2(v[8 * e + 4], v[8 * e + 5]), pack2(v[8 * e + 6], v[8 * e + 7]));
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = 8 * x + (lane >> 2), ch = lane & 3, row = sub * 32 + r;
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+            const int tk = static_cast<int>((row * ginv) >> 16);
+            if (row < rows)
+              *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(tk) * a.hq + (row - tk * g)) * D + c + 8 * ch) = w;
           }
-        }
-      };
-      if (two && my > 0) {
-#pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-          uint32_t ov[32];
-          float v[32];
-          tmem_ld_x32(o_tmem + 32 * c, ov);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = empty ? 0.f : __uint_as_float(ov[e]) * w_own;
-          emit(c, v);
-        }
-      } else {
-        for (int c = c0; c < c0 + nc; ++c) {
-          uint32_t ov[32];
-          float v[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.f;
-          if (my > 0) {
-            tmem_ld_x32(o_tmem + 32 * c, ov);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = empty ? 0.f : __uint_as_float(ov[e]) * w_own;
-          }
-          if (!two && n_other > 0) {
-            tmem_ld_x32(o_oth + 32 * c, ov);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] += empty ? 0.f : __uint_as_float(ov[e]) * w_oth;
-          }
-          emit(c, v);
         }
       }
-      if (pc.part >= 0) {
-        if (valid && (two || t == 0)) a.part_lse[prow] = lse;
-      } else {
-        if (valid && (two || t == 0) && a.lse)
-          a.lse[(static_cast<int64_t>(pc.row0) + tok) * a.hq + kvh * g + rl % g] = lse;
+      if (odd) {
+        // columns with a non-finite value that this row sees: what the sum would be
         __syncwarp();
-        const int per = 4 * nc;           // 16-byte chunks of a row here: a power of two
-        const int rows_per = 32 / per;    // rows per store of the warp
-        const uint32_t ginv = 65536u / g + 1;   // row / g for rows below 128, g <= 64: exact
-        const int ch = 4 * c0 + lane % per, r0 = lane / per;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) +
-                             (static_cast<int64_t>(pc.row0) * a.hq + kvh * g) * D + 8 * ch;
-        const int last = min(tpt * g, (pc.q_len - tok_t) * g);   // rows of this tile
-#pragma unroll 4
-        for (int k = 0; k < per; ++k) {
-          const int r = r0 + k * rows_per, row = sub * 32 + r;
-          const uint4 x = *reinterpret_cast<const uint4*>(stage + r * D * 2 + ((ch ^ (r & 7)) << 4));
-          const int tk = static_cast<int>((row * ginv) >> 16);
-          if (row < last)
-            *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(tok_t + tk) * a.hq + (row - tk * g)) * D) = x;
+        const unsigned long long tag = static_cast<unsigned long long>(~static_cast<uint32_t>(k + 1)) << 32;
+        auto seen = [&](int kind, int col) {
+          const unsigned long long x = bars->first[k & 1][kind][col];
+          return (x & 0xffffffff00000000ull) == tag && static_cast<int>(x & 0xffffffffu) <= lim;
+        };
+        for (int c = c_lo; valid && c < c_hi; ++c) {
+          const bool pos = seen(0, c), neg = seen(1, c), nan = seen(2, c) || (pos && neg);
+          if (!pos && !neg && !nan) continue;
+          const float add = nan ? __int_as_float(0x7fc00000) : pos ? INFINITY : -INFINITY;
+          if (pc.part >= 0) {
+            a.part_o[prow * D + c] += add;
+          } else {
+            __nv_bfloat16* x = out + (static_cast<int64_t>(rt) * a.hq + rh) * D + c;
+            *x = __float2bfloat16_rn(__bfloat162float(*x) + add);
+          }
         }
       }
+      tc_fence_before();
+      mbar_arrive(&bars->done[k & 1]);   // O and the notes have been read
     }
+    if (!ok) fail(9);
   }
   tc_fence_before();
   __syncthreads();
@@ -646,7 +745,7 @@ int launch_tc(const AttendArgs& a, cudaStream_t s) {
   if (cudaFuncSetAttribute(attend_tc_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
       cudaSuccess)
     return PA_ERR_CUDA;
-  return launch_overlapped(attend_tc_kernel<D, PAGED>, dim3(tile_blocks(a)), 384, C::SMEM_BYTES, s, mq, mk, mv, p);
+  return launch_overlapped(attend_tc_kernel<D, PAGED>, dim3(tile_blocks(a) < kSms ? tile_blocks(a) : kSms), 384, C::SMEM_BYTES, s, mq, mk, mv, p);
 }
 
 }  // namespace
