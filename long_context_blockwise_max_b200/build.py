@@ -1,6 +1,8 @@
 """Build step of the native library: compiles csrc/*.cu for sm_100a into
 ``libpulsar_b200.so`` beside this file (in-tree, so it travels with the
-source tree).  Runs on a machine without a GPU: nvcc cross-compiles.
+source tree), and the serving operators' Python call layer (csrc/*.cpp, against
+torch's headers) into ``_serving_call.so``.  Runs on a machine without a GPU:
+nvcc cross-compiles.
 
     python -m long_context_blockwise_max_b200.build [--force] [--verbose]
 """
@@ -16,6 +18,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libpulsar_b200.so")
+CALL_SRC = os.path.join(CSRC, "serving_call.cpp")
+CALL = os.path.join(PKG, "_serving_call.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -47,10 +51,38 @@ def _compile(src: str, obj: str, ptxas_verbose: bool) -> subprocess.CompletedPro
     return subprocess.run(cmd, capture_output=True, text=True)
 
 
+def build_call_layer(force: bool = False) -> str:
+    """Compile the Python call layer of the serving operators if a source or
+    header of it is newer; return its path.  Links to the library built by
+    ``build`` (found beside it at run time)."""
+    deps = [CALL_SRC] + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    if not force and os.path.exists(CALL) and all(os.path.getmtime(p) <= os.path.getmtime(CALL) for p in deps):
+        return CALL
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    lib = os.path.join(base, "lib")
+    tmp = CALL + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in inc), CALL_SRC,
+           "-o", tmp, f"-L{PKG}", "-l:" + os.path.basename(LIB), f"-L{lib}", "-ltorch_python", "-ltorch_cuda",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("compiling the call layer failed")
+    os.replace(tmp, CALL)
+    return CALL
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     """Compile the library if a source is newer than it; return its path.
     Each .cu is compiled to an object in parallel under _build/, then linked."""
     if not force and not _stale():
+        build_call_layer()
         return LIB
     from concurrent.futures import ThreadPoolExecutor
     bdir = os.path.join(ROOT, "_build")
@@ -74,6 +106,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("nvcc link failed")
     os.replace(tmp, LIB)
+    build_call_layer(force)
     return LIB
 
 

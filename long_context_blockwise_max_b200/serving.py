@@ -14,6 +14,8 @@ devices are checked here, missing outputs and workspaces allocated with torch,
 and raw pointers passed to the C entry point of the same name, on the tensors'
 device and its current stream.  No call waits for the GPU (unless
 ``pulsar.set_status_checks`` is on), so each may be captured into a CUDA graph.
+An ordinary call (missing outputs, tensors on the current device) goes through
+the compiled call layer ``_serving_call``, which does the same in less time.
 """
 from __future__ import annotations
 
@@ -23,7 +25,12 @@ from functools import lru_cache
 import torch
 
 from . import pulsar
-from .pulsar import _check, _dtype_code, _lib, _need, _same
+from .pulsar import PulsarError, _check, _dtype_code, _lib, _need, _same
+
+try:
+    from . import _serving_call as _ordinary
+except ImportError as e:
+    raise ImportError(f"{e}; run `python -m long_context_blockwise_max_b200.build`") from e
 
 # Every symbol declared in include/pulsar_serving.h.
 ABI_SYMBOLS = (
@@ -132,6 +139,15 @@ def _call(fn, ref: torch.Tensor, ws, *args):
         _check(rc, fn.__name__, ws)
 
 
+def _answer(got, name: str):
+    """The outputs of an ordinary call, or its error."""
+    if type(got) is int:
+        raise PulsarError(got, name)
+    if pulsar._STATUS_CHECKS:
+        _check(0, name, got[-1])
+    return got
+
+
 def pa_paged_schedule(q_len, kv_len, block_table, free_pages, page_size: int, n_tokens: int, cu_q=None,
                       kv_len_out=None, positions=None, slots=None, n_used=None, ws=None):
     """Page tables, slot map and positions of one step.  ``q_len``, ``kv_len``
@@ -139,6 +155,10 @@ def pa_paged_schedule(q_len, kv_len, block_table, free_pages, page_size: int, n_
     is extended in place from the front of ``free_pages``.  ``n_tokens``: rows
     of the step's tensors (at least sum(q_len); rows behind it get slot -1).
     Returns (cu_q, kv_len_out, positions, slots, n_used, ws)."""
+    if cu_q is None and kv_len_out is None and positions is None and slots is None and n_used is None and ws is None:
+        got = _ordinary.paged_schedule(q_len, kv_len, block_table, free_pages, page_size, n_tokens)
+        if got is not None:
+            return _answer(got, "pa_paged_schedule")
     _on(q_len, kv_len, block_table, free_pages, cu_q, kv_len_out, positions, slots, n_used, ws)
     B, n_tokens = q_len.numel(), int(n_tokens)
     _ints((("q_len", q_len), ("kv_len", kv_len), ("kv_len_out", kv_len_out)), B)
@@ -183,6 +203,10 @@ def pa_paged_append(q, k_new, v_new, positions, slots, k_pages, v_pages, rope_th
     ``v_pages`` None: nothing is written; negative slots are skipped).  Returns
     (rotated q or None, rotated k or None, ws); ``want_k`` or ``k_out`` asks
     for k."""
+    if q_out is None and k_out is None and ws is None:
+        got = _ordinary.paged_append(q, k_new, v_new, positions, slots, k_pages, v_pages, rope_theta, want_k)
+        if got is not None:
+            return _answer(got, "pa_paged_append")
     _on(k_new, q, v_new, positions, slots, k_pages, v_pages, q_out, k_out, ws)
     ldk = _rows(k_new, "k_new")
     N, hkv, d = k_new.shape
@@ -253,6 +277,10 @@ def pa_prompt_attend(q, k, v, cu_q, o=None, lse=None, want_lse: bool = True, ws=
     ``cu_q[b + 1] - 1`` of ``q`` [N][hq][d], ``k`` and ``v`` [N][hkv][d]
     (rotated) are prompt b.  Rows behind the last prompt are left as they
     were.  Returns (o, lse or None, ws)."""
+    if o is None and lse is None and ws is None:
+        got = _ordinary.prompt_attend(q, k, v, cu_q, want_lse)
+        if got is not None:
+            return _answer(got, "pa_prompt_attend")
     _on(q, k, v, cu_q, o, lse, ws)
     ldq = _rows(q, "q")
     N, hq, d = q.shape
@@ -283,6 +311,10 @@ def pa_paged_attend(q, cu_q, kv_len, block_table, k_pages, v_pages, max_q: int, 
     are in the cache already); ``max_q`` bounds the new tokens of a request.
     Rows behind the last request are left as they were.  Returns (o, lse or
     None, ws)."""
+    if o is None and lse is None and ws is None:
+        got = _ordinary.paged_attend(q, cu_q, kv_len, block_table, k_pages, v_pages, max_q, want_lse)
+        if got is not None:
+            return _answer(got, "pa_paged_attend")
     _on(q, cu_q, kv_len, block_table, k_pages, v_pages, o, lse, ws)
     ldq = _rows(q, "q")
     N, hq, d = q.shape
