@@ -2,6 +2,8 @@
 // kernel arguments, the work plan of an attention call and the launchers.
 #pragma once
 
+#include <atomic>
+
 #include "pa_internal.h"
 #include "../../include/pulsar_serving.h"
 
@@ -38,6 +40,7 @@ struct AppendArgs {
   int64_t n_slots;
   void *q_out, *k_out;
   DeviceStatus* status;
+  int small;   // few tokens: the first block clears the status and checks every slot
 };
 int launch_paged_append(const AppendArgs& a, cudaStream_t s);
 
@@ -58,11 +61,17 @@ struct MergeItem {
   int32_t part0, n_parts;
 };
 
-// Start of one block's range of decode work: request, kv head and key group
-// of its first unit, and the units in all.
+// One block's range of decode work, all that it has to know to start: the
+// request, kv head and key group of its first unit, and how the units are
+// shared out.
 struct DecodeStart {
-  int32_t b, kvh, unit, pad;
+  int32_t b, kvh, unit, n_units;     // n_units: key groups of that request
+  int32_t kv, q, row0, steps;        // its lengths; units of this block
+  int64_t first;                     // this block's first unit
+  int64_t each;                      // units per block; the first `more` blocks have one more
+  int32_t more, pad[3];
 };
+static_assert(sizeof(DecodeStart) == 64, "four 16-byte loads");
 
 struct PlanHead {
   int32_t n_pieces;     // pieces of the tile kernels, per kv head
@@ -71,7 +80,6 @@ struct PlanHead {
   int32_t heads_inner;  // order of the tile kernels' work (piece_at)
   uint32_t next;        // units of work taken beyond each block's first
   int32_t pad;
-  int64_t decode_units; // key groups of the decode kernel, over kv heads
 };
 
 struct AttendArgs {
@@ -148,10 +156,29 @@ int launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// Sets a kernel's dynamic shared memory once per device.
+template <auto* kernel>
+int allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (set.load(std::memory_order_relaxed) & bit)) return PA_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  set.fetch_or(bit, std::memory_order_relaxed);
+  return PA_OK;
+}
+
 // Units of work of a tile kernel: the most pieces the arguments allow, times kv heads.
 inline unsigned tile_blocks(const AttendArgs& a) {
   return static_cast<unsigned>(a.piece_cap) * static_cast<unsigned>(a.hkv);
 }
+
+// TMA map (a CUtensorMap; serving_tc.cu) of a 16-bit tensor
+// [rows][heads][d] with a row stride of ld elements, boxes of 64 columns x
+// `box_heads` x `box_rows`, 128-byte swizzle.
+bool rows_map(void* map, const void* base, int64_t rows, int heads, int d, int64_t ld, int box_heads, int box_rows);
 
 #ifdef __CUDACC__
 // Piece and kv head of the i-th unit of work (of n_pieces * hkv).  Units that

@@ -88,8 +88,6 @@ int pa_paged_schedule(const int32_t* q_len, const int32_t* kv_len, int32_t B, in
   if (n_tokens > 0 && (!positions || !slots)) return PA_ERR_INVALID;
   rc = check_ws(ws, ws_bytes, kStatusBytes);
   if (rc) return rc;
-  rc = clear_status(ws, s);
-  if (rc) return rc;
   ScheduleArgs a;
   a.q_len = q_len; a.kv_len = kv_len; a.B = B;
   a.block_table = block_table; a.table_stride = table_stride; a.max_pages = max_pages;
@@ -128,9 +126,7 @@ int pa_paged_append(const void* q, const void* k, const void* v, int dtype, int6
     if (p && !aligned(p, 16)) return PA_ERR_UNSUPPORTED;
   rc = check_ws(ws, ws_bytes, kStatusBytes);
   if (rc) return rc;
-  rc = clear_status(ws, s);
-  if (rc) return rc;
-  if (N == 0) return PA_OK;
+  if (N == 0) return clear_status(ws, s);
   AppendArgs a;
   a.q = q; a.k = k; a.v = v; a.dtype = dtype;
   a.N = N; a.ldq = ldq; a.ldk = ldk; a.ldv = ldv;
@@ -139,6 +135,7 @@ int pa_paged_append(const void* q, const void* k, const void* v, int dtype, int6
   a.k_pages = k_pages; a.v_pages = v_pages; a.n_slots = n_slots;
   a.q_out = q_out; a.k_out = k_out_opt;
   a.status = static_cast<DeviceStatus*>(ws);
+  a.small = N <= 4096;
   return launch_paged_append(a, s);
 }
 

@@ -8,9 +8,11 @@
 // whatever the lengths, so that no SM waits for the longest request.
 //
 // Each of the 4 warps takes 32 keys of a group and streams them through its
-// own 3-stage cp.async ring.  The ring runs across the ends of requests and
-// heads: the copies of the next range are in flight while a finished one is
-// merged.  A key's page is looked up one group ahead of its copy.
+// own 3-stage ring of TMA copies (one box per page or 32 keys and 64 columns;
+// copies by the warps' own 16-byte accesses kept each warp busy for a third of
+// a tile's time).  The ring runs across the ends of requests and heads: the
+// copies of the next range are in flight while a finished one is merged.  A
+// key's page is looked up one group ahead of its copy.
 //
 // With at most 8 rows, the probabilities go in as a bf16 pair, high part in
 // MMA rows 0-7 and residual in rows 8-15, at no extra MMA; with 9 to 16 rows
@@ -20,8 +22,11 @@
 // workspace; the last block to arrive merges them in block order, so results
 // do not depend on which block that is.
 #include "serving.h"
+#include "sm100.cuh"
 
 namespace pa {
+using namespace sm100;
+
 
 namespace {
 
@@ -33,15 +38,6 @@ static_assert(kWarps * kKT == kPlanTile, "a block's step is one planned key grou
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;   // 0: fill the 16 bytes with zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
@@ -64,22 +60,24 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 template <int D>
 struct DecCfg {
   static constexpr int CH = D / 8;                    // 16-byte chunks per key row
-  static constexpr int ROWB = D * 2;
-  static constexpr int TILE = kKT * ROWB;             // K (or V) tile bytes
+  static constexpr int NKB = D / 64;                  // column blocks of 32 keys x 128 B
+  static constexpr int KB = kKT * 128;
+  static constexpr int TILE = NKB * KB;               // K (or V) tile bytes
   static constexpr int STAGE = 2 * TILE;              // K + V
   static constexpr int RING = kStages * STAGE;        // per warp
   static constexpr int OFF_RED = kWarps * RING;       // [warp][16][D] floats
   static constexpr int OFF_ML = OFF_RED + kWarps * 16 * D * 4;   // [2][warp][16] floats
   static constexpr int OFF_BAD = OFF_ML + 2 * kWarps * 16 * 4;   // [3][D] first key with +inf, -inf, NaN
-  static constexpr int OFF_FLAG = OFF_BAD + 3 * D * 4;
-  static constexpr int SMEM = OFF_FLAG + 16;
+  static constexpr int OFF_BAR = OFF_BAD + 3 * D * 4;            // [warp][stage] copies have landed
+  static constexpr int OFF_FLAG = OFF_BAR + kWarps * kStages * 8;
+  static constexpr int SMEM = OFF_FLAG + 16 + 768;    // the base is aligned to 1024 bytes (it is to 256 already)
   static constexpr float SCALE = static_cast<float>(kLog2e / (D == 128 ? 11.31370849898476039 : 8.0));
 };
 
-// byte offset of (key row, 16-byte chunk) inside a swizzled tile
+// byte offset of (key row, 16-byte chunk) inside a tile (128-byte swizzle)
 template <int D>
 __device__ __forceinline__ uint32_t swz(int key, int chunk) {
-  return key * DecCfg<D>::ROWB + ((chunk ^ (key & 7)) << 4);
+  return (chunk >> 3) * DecCfg<D>::KB + key * 128 + (((chunk & 7) ^ (key & 7)) << 4);
 }
 
 // A place in the row of key groups: request, kv head, group of that pair.
@@ -112,69 +110,73 @@ struct Cursor {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                                       const __grid_constant__ CUtensorMap tmV,
+                                                                       const __grid_constant__ AttendArgs a,
+                                                                       int box_rows, int oob_row) {
   using C = DecCfg<D>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_dep_wait();
-  grid_dep_launch();
-  const int64_t total = a.head->decode_units;
-  const int64_t each = total / gridDim.x, more = total % gridDim.x;
-  auto first_unit = [&](int64_t c) { return c * each + (c < more ? c : more); };
-  auto block_of = [&](int64_t u) {   // the block whose range holds group u
-    return u < more * (each + 1) ? u / (each + 1) : more + (u - more * (each + 1)) / each;
-  };
-  const int64_t u_lo = first_unit(blockIdx.x);
-  const int steps = static_cast<int>(first_unit(blockIdx.x + 1) - u_lo);
-  if (steps == 0) return;
-  const int64_t max_kv = static_cast<int64_t>(a.max_pages) * a.page_size;
-  const int g = a.hq / a.hkv;
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::RING;
+  uint8_t* ring = smem + warp * C::RING;
   float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
   float* red_m = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* red_l = red_m + kWarps * 16;
   int* bad = reinterpret_cast<int*>(smem + C::OFF_BAD);
-  volatile int* flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);   // [0] non-finite V, [1] last to arrive
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * kStages;
+  // [0] non-finite V, [1] last to arrive, [2] a wait ran out
+  volatile int* flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);
   for (int i = threadIdx.x; i < 3 * D; i += kWarps * 32) bad[i] = INT32_MAX;
-  if (threadIdx.x == 0) flag[0] = 0;
+  if (threadIdx.x == 0) flag[0] = flag[2] = 0;
+  if (lane == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
   __syncthreads();
+  grid_dep_wait();      // the set-up above overlaps the plan
+  grid_dep_launch();
 
   const DecodeStart ds = a.starts[blockIdx.x];
-  Cursor ahead;                 // the copies' place: the next group to be issued
-  ahead.b = ds.b;
-  ahead.kvh = ds.kvh;
-  ahead.unit = ds.unit;
-  ahead.load(a);
-  Cursor cur = ahead;           // the computation's place
-  const int64_t key_stride = static_cast<int64_t>(a.hkv) * D;
-  const __nv_bfloat16* Kg = static_cast<const __nv_bfloat16*>(a.n_slots > 0 ? a.k : a.q);
-  const __nv_bfloat16* Vg = static_cast<const __nv_bfloat16*>(a.n_slots > 0 ? a.v : a.q);
-  // slot of this lane's key in the group at `ahead` (the next to be issued)
-  auto look_up = [&]() -> int64_t {
-    const int64_t key = static_cast<int64_t>(ahead.unit) * kPlanTile + warp * kKT + lane;
-    return key < ahead.kv ? key_slot(a, ahead.b, key) : -1;
+  const int steps = ds.steps;
+  if (steps == 0) return;
+  const int64_t u_lo = ds.first;
+  auto block_of = [&](int64_t u) {   // the block whose range holds group u
+    const int64_t cut = ds.more * (ds.each + 1);
+    return u < cut ? u / (ds.each + 1) : ds.more + (u - cut) / ds.each;
   };
-  int64_t slot = look_up();
+  const int64_t max_kv = static_cast<int64_t>(a.max_pages) * a.page_size;
+  const int g = a.hq / a.hkv;
+  Cursor ahead = {ds.b, ds.kvh, ds.unit, ds.n_units, ds.kv, ds.q, ds.row0};   // the next group to be issued
+  Cursor cur = ahead;                                                         // the computation's place
+  // row coordinate of this lane's box of the group at `ahead`
+  const int nbox = kKT / box_rows;
+  auto look_up = [&]() -> int {
+    const int64_t key = static_cast<int64_t>(ahead.unit) * kPlanTile + warp * kKT + lane * box_rows;
+    if (lane >= nbox || key >= ahead.kv) return oob_row;
+    const int64_t slot = key_slot(a, ahead.b, key);
+    return slot < 0 ? oob_row : static_cast<int>(slot);
+  };
+  int row = look_up();
+  int issued = 0;
   auto issue = [&](int it) {
-    if (it < steps) {
-      const uint32_t base = ring + (it % kStages) * C::STAGE;
-      const int mine = static_cast<int>(slot);
-      const int64_t head = static_cast<int64_t>(ahead.kvh) * D;
+    if (it >= steps || flag[2]) return;
+    ++issued;
+    uint8_t* dst = ring + (it % kStages) * C::STAGE;
+    uint64_t* bar = &full[it % kStages];
+    if (lane == 0) mbar_arrive_expect_tx(bar, C::STAGE);
+    __syncwarp();
+    if (lane < nbox)
 #pragma unroll
-      for (int e = 0; e < C::CH; ++e) {
-        const int idx = e * 32 + lane;
-        const int key = idx / C::CH, ch = idx % C::CH;
-        const int at = __shfl_sync(0xffffffffu, mine, key);
-        const int64_t off = at >= 0 ? at * key_stride + head + ch * 8 : 0;
-        cp_async16(base + swz<D>(key, ch), Kg + off, at >= 0);
-        cp_async16(base + C::TILE + swz<D>(key, ch), Vg + off, at >= 0);
+      for (int kb = 0; kb < C::NKB; ++kb) {
+        tma_load_3d(dst + kb * C::KB + lane * box_rows * 128, &tmK, bar, kb * 64, ahead.kvh, row);
+        tma_load_3d(dst + C::TILE + kb * C::KB + lane * box_rows * 128, &tmV, bar, kb * 64, ahead.kvh, row);
       }
-      if (it + 1 < steps) {
-        ahead.step(a, max_kv);
-        slot = look_up();
-      }
+    if (it + 1 < steps) {
+      ahead.step(a, max_kv);
+      row = look_up();
     }
-    cp_async_commit();
   };
 
   const int qi = lane >> 2, qc = (lane & 3) * 2;
@@ -212,21 +214,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(AttendArg
   begin();
   for (int it = 0; it < steps; ++it) {
     issue(it + kStages - 1);
-    cp_async_wait<kStages - 1>();
+    const int st = it % kStages;
+    if (!mbar_wait(&full[st], (it / kStages) & 1, flag + 2, a.wait_limit_ns, &a.head->abort)) {
+      // every warp keeps to its steps (they share barriers), on whatever is there
+      flag[2] = 1;
+      a.head->abort = 1;
+      set_status(a.status, PA_ERR_TIMEOUT, static_cast<int>(blockIdx.x), warp);
+    }
     __syncwarp();
-    const uint32_t sK = ring + (it % kStages) * C::STAGE;
+    const uint32_t sK = smem_u32(ring + st * C::STAGE);
     const uint32_t sV = sK + C::TILE;
     const int key0 = cur.unit * kPlanTile + warp * kKT;
     if (key0 < cur.kv) {
       const bool edge = key0 + kKT - 1 > ctx;   // some row does not see some key of this tile
-      if (edge && cur.q > 1) {
-        // V of keys that not every row sees: a non-finite value is taken
-        // out of the product and noted (the rows that see it get it at the end)
-        uint8_t* v = smem + warp * C::RING + (it % kStages) * C::STAGE + C::TILE;
+      if (edge) {
+        // V of keys that not every row sees: rows without a key are zeroed,
+        // and a non-finite value is taken out of the product and noted (the
+        // rows that see it get it at the end)
+        uint8_t* v = ring + st * C::STAGE + C::TILE;
         for (int i = lane; i < kKT * C::CH; i += 32) {
           const int key = key0 + i / C::CH, c = i % C::CH;
-          if (key <= ctx || key >= cur.kv) continue;
-          uint16_t* e = reinterpret_cast<uint16_t*>(v + swz<D>(i / C::CH, c));
+          if (key <= ctx) continue;
+          uint4* chunk = reinterpret_cast<uint4*>(v + swz<D>(i / C::CH, c));
+          if (key >= cur.kv) {
+            *chunk = make_uint4(0, 0, 0, 0);
+            continue;
+          }
+          uint16_t* e = reinterpret_cast<uint16_t*>(chunk);
           for (int k = 0; k < 8; ++k)
             if ((e[k] & 0x7f80) == 0x7f80) {
               atomicMin(&bad[((e[k] & 0x7f) ? 2 : (e[k] >> 15)) * D + 8 * c + k], key);
@@ -234,6 +248,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(AttendArg
               e[k] = 0;
             }
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the next copy into this stage
         __syncwarp();
       }
       // S = Q K^T over 32 keys: 4 n8 tiles
@@ -270,16 +285,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(AttendArg
       const float sub0 = t0 == -INFINITY ? 0.f : t0 * C::SCALE, sub1 = t1 == -INFINITY ? 0.f : t1 * C::SCALE;
       const float al0 = fast_exp2(m0 * C::SCALE - sub0);
       const float al1 = pair ? al0 : fast_exp2(m1 * C::SCALE - sub1);
+      const bool grew = t0 != m0 || (!pair && t1 != m1);
       m0 = t0;
       m1 = t1;
-      l0 *= al0;
-      l1 *= al1;
+      if (__any_sync(0xffffffffu, grew)) {
+        l0 *= al0;
+        l1 *= al1;
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        o[j][0] *= al0;
-        o[j][1] *= al0;
-        o[j][2] *= al1;
-        o[j][3] *= al1;
+        for (int j = 0; j < D / 8; ++j) {
+          o[j][0] *= al0;
+          o[j][1] *= al0;
+          o[j][2] *= al1;
+          o[j][3] *= al1;
+        }
       }
       uint32_t pf[2][4];        // P as A fragments, two k16 steps
 #pragma unroll
@@ -438,16 +456,30 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(AttendArg
       begin();
     }
   }
-  cp_async_wait<0>();
+  // Every copy has been waited for; after a wait that ran out, once more.
+  if (flag[2]) {
+    int zero = 0;
+    for (int it = max(0, issued - kStages); it < issued; ++it)
+      mbar_wait(&full[it % kStages], (it / kStages) & 1, &zero, a.wait_limit_ns);
+  }
 }
 
 template <int D>
 int launch(const AttendArgs& a, cudaStream_t s) {
   constexpr int smem = DecCfg<D>::SMEM;
   static_assert(smem <= 232448, "shared memory of one block");
-  if (cudaFuncSetAttribute(attend_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  const int rc = allow_smem<attend_decode_kernel<D>>(smem);
+  if (rc != PA_OK) return rc;
+  // (an empty cache has no page to read: every box is out of range, and the
+  // maps are made over q only to have an address)
+  const int64_t rows = a.n_slots > 0 ? a.n_slots : 1;
+  const int box = a.page_size < kKT ? a.page_size : kKT;
+  CUtensorMap mk, mv;
+  if (!rows_map(&mk, a.n_slots > 0 ? a.k : a.q, rows, a.hkv, D, a.ldk, 1, box) ||
+      !rows_map(&mv, a.n_slots > 0 ? a.v : a.q, rows, a.hkv, D, a.ldv, 1, box))
     return PA_ERR_CUDA;
-  return launch_overlapped(attend_decode_kernel<D>, dim3(a.decode_ctas), kWarps * 32, smem, s, a);
+  return launch_overlapped(attend_decode_kernel<D>, dim3(a.decode_ctas), kWarps * 32, smem, s, mk, mv, a, box,
+                           static_cast<int>(rows));
 }
 
 }  // namespace

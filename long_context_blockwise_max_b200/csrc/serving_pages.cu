@@ -27,6 +27,9 @@ __global__ void __launch_bounds__(1024) paged_schedule_kernel(ScheduleArgs a) {
   __shared__ int64_t tmp[2][64];
   __shared__ int32_t used;
   const int shift = a.page_shift, page = 1 << shift;
+  grid_dep_wait();
+  // one block: it clears the status itself (more have it cleared before them)
+  if (gridDim.x == 1 && threadIdx.x < kStatusBytes / 4) reinterpret_cast<int32_t*>(a.status)[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     cu[0] = 0;
     pages[0] = 0;
@@ -116,6 +119,14 @@ __global__ void __launch_bounds__(256) paged_append_kernel(AppendArgs a, RopeFre
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tpb;
   const int nt = static_cast<int>(min(static_cast<int64_t>(tpb), a.N - t0));
   const bool rope = a.rope_theta != 0.0;
+  grid_dep_wait();
+  if (a.small && blockIdx.x == 0) {
+    if (threadIdx.x < kStatusBytes / 4) reinterpret_cast<int32_t*>(a.status)[threadIdx.x] = 0;
+    __syncthreads();
+    if (a.slots)
+      for (int64_t t = threadIdx.x; t < a.N; t += 256)
+        if (a.slots[t] >= a.n_slots) set_status(a.status, PA_ERR_INVALID, static_cast<int>(t), a.slots[t]);
+  }
   if (rope) {
     for (int e = threadIdx.x; e < nt * half; e += 256) {
       const double x = a.positions[t0 + e / half] * turns.omega[e % half];   // angle in turns
@@ -136,7 +147,7 @@ __global__ void __launch_bounds__(256) paged_append_kernel(AppendArgs a, RopeFre
     const int64_t tok = t0 + t;
     int64_t slot = a.slots ? a.slots[tok] : -1;
     if (slot >= a.n_slots) {
-      if (i == 0) set_status(a.status, PA_ERR_INVALID, static_cast<int>(tok), static_cast<int>(slot));
+      if (i == 0 && !a.small) set_status(a.status, PA_ERR_INVALID, static_cast<int>(tok), static_cast<int>(slot));
       slot = -1;
     }
     const T* src;
@@ -183,18 +194,18 @@ __global__ void __launch_bounds__(256) paged_append_kernel(AppendArgs a, RopeFre
 
 int launch_paged_schedule(const ScheduleArgs& a, cudaStream_t s) {
   const size_t smem = 13 * static_cast<size_t>(a.B) + 8;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(paged_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return PA_ERR_CUDA;
+  if (smem > 46 * 1024) {   // beside 1 KB of static arrays
+    const int rc = allow_smem<paged_schedule_kernel>(13 * kMaxRequests + 8);
+    if (rc != PA_OK) return rc;
+  }
   // one thread per token up to a block per SM; a small step's block has no
   // more threads than its requests and tokens need
   const int64_t most = a.n_tokens > a.B ? a.n_tokens : a.B;
   const int threads = most <= 256 ? 256 : 1024;
   const int64_t want = (a.n_tokens + threads - 1) / threads;
   const int grid = static_cast<int>(want < 1 ? 1 : want > kSms ? kSms : want);
-  paged_schedule_kernel<<<grid, threads, smem, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (grid > 1 && cudaMemsetAsync(a.status, 0, kStatusBytes, s) != cudaSuccess) return PA_ERR_CUDA;
+  return launch_overlapped(paged_schedule_kernel, dim3(grid), threads, smem, s, a);
 }
 
 int launch_paged_append(const AppendArgs& a, cudaStream_t s) {
@@ -205,11 +216,10 @@ int launch_paged_append(const AppendArgs& a, cudaStream_t s) {
   const int tpb = a.N >= 8 * kSms ? 4 : 1;
   const int64_t grid = (a.N + tpb - 1) / tpb;
   const size_t smem = sizeof(float2) * tpb * (a.d / 2);
-  if (a.dtype == PA_F32)
-    paged_append_kernel<float><<<static_cast<unsigned>(grid), 256, smem, s>>>(a, f, tpb);
-  else
-    paged_append_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), 256, smem, s>>>(a, f, tpb);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (!a.small && cudaMemsetAsync(a.status, 0, kStatusBytes, s) != cudaSuccess) return PA_ERR_CUDA;
+  const dim3 blocks(static_cast<unsigned>(grid));
+  return a.dtype == PA_F32 ? launch_overlapped(paged_append_kernel<float>, blocks, 256, smem, s, a, f, tpb)
+                           : launch_overlapped(paged_append_kernel<__nv_bfloat16>, blocks, 256, smem, s, a, f, tpb);
 }
 
 }  // namespace pa

@@ -65,6 +65,7 @@ __device__ __forceinline__ void put_piece(const AttendArgs& a, int at, int b, co
 // One block.  Latency-bound (loads of the lengths, one scan, bisections in
 // shared memory): its time is on the critical path of every call.
 __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t max_kv) {
+  grid_dep_wait();     // the lengths, and the workspace's last use
   grid_dep_launch();
   extern __shared__ __align__(16) uint8_t raw[];
   int64_t* units = reinterpret_cast<int64_t*>(raw);               // [B + 1] decode key groups before request b
@@ -120,15 +121,22 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     const int64_t each = unit_base / a.decode_ctas, more = unit_base % a.decode_ctas;
     for (int c = tid; c < a.decode_ctas; c += threads) {
       const int64_t u0 = c * each + (c < more ? c : more);
-      DecodeStart st = {0, 0, 0, 0};
+      int4 x = make_int4(0, 0, 0, 1), y = make_int4(0, 0, 0, static_cast<int>(each + (c < more)));
       if (u0 < unit_base) {
-        st.b = upper_index(units, a.B + 1, u0);
-        const int groups = static_cast<int>((units[st.b + 1] - units[st.b]) / a.hkv);
-        const int64_t rem = u0 - units[st.b];
-        st.kvh = static_cast<int>(rem / groups);
-        st.unit = static_cast<int>(rem % groups);
+        const int b = upper_index(units, a.B + 1, u0);
+        const Lens r = lens_of(a, b, max_kv, false);
+        const int groups = static_cast<int>((units[b + 1] - units[b]) / a.hkv);
+        const int64_t rem = u0 - units[b];
+        x = make_int4(b, static_cast<int>(rem / groups), static_cast<int>(rem % groups), groups);
+        y.x = static_cast<int>(r.kv);
+        y.y = static_cast<int>(r.q);
+        y.z = static_cast<int>(r.row0);
       }
-      *reinterpret_cast<int4*>(a.starts + c) = make_int4(st.b, st.kvh, st.unit, 0);
+      int4* dst = reinterpret_cast<int4*>(a.starts + c);
+      dst[0] = x;
+      dst[1] = y;
+      *reinterpret_cast<longlong2*>(dst + 2) = make_longlong2(u0, each);
+      dst[3] = make_int4(static_cast<int>(more), 0, 0, 0);
     }
   }
   // ---- tiles --------------------------------------------------------------
@@ -257,7 +265,6 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     a.head->abort = 0;
     a.head->next = 0;
     a.head->heads_inner = static_cast<double>(keys) * a.hkv * a.d * (a.dtype == PA_BF16 ? 4 : 8) <= kL2Keys;
-    a.head->decode_units = unit_base;
   }
 }
 
@@ -390,13 +397,12 @@ size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws) {
 int launch_attend(const AttendArgs& a, cudaStream_t s) {
   const int64_t max_kv = a.block_table ? static_cast<int64_t>(a.max_pages) * a.page_size : a.N;
   const size_t smem = (sizeof(int64_t) + sizeof(int32_t)) * (static_cast<size_t>(a.B) + 1);
-  if (smem > 32 * 1024 &&   // beside 14 KB of static arrays
-      cudaFuncSetAttribute(attend_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return PA_ERR_CUDA;
-  attend_plan_kernel<<<1, plan_threads(a), smem, s>>>(a, max_kv);
-  if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
-  int rc = PA_OK;
+  if (smem > 32 * 1024) {   // beside 14 KB of static arrays
+    const int rc = allow_smem<attend_plan_kernel>(12 * (kMaxRequests + 1));
+    if (rc != PA_OK) return rc;
+  }
+  int rc = launch_overlapped(attend_plan_kernel, dim3(1), plan_threads(a), smem, s, a, max_kv);
+  if (rc != PA_OK) return rc;
   profile_begin(s);
   if (a.decode_ctas > 0) rc = launch_attend_decode(a, s);
   if (rc == PA_OK && a.tiles) rc = a.dtype == PA_BF16 ? launch_attend_tc(a, s) : launch_attend_simt(a, s);

@@ -194,9 +194,8 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
 template <typename T, int D, int ROWS>
 int launch(const AttendArgs& a, cudaStream_t s) {
   constexpr int smem = SimtCfg<D, ROWS>::SMEM;
-  if (cudaFuncSetAttribute(attend_simt_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess)
-    return PA_ERR_CUDA;
+  const int rc = allow_smem<attend_simt_kernel<T, D, ROWS>>(smem);
+  if (rc != PA_OK) return rc;
   return launch_overlapped(attend_simt_kernel<T, D, ROWS>, dim3(tile_blocks(a)), 256, smem, s, a);
 }
 

@@ -702,28 +702,6 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
   }
 }
 
-// 16-bit tensor [rows][heads][d] with a row stride of ld elements, boxes of
-// 64 columns x `box_heads` x `box_rows`, 128-byte swizzle.
-bool rows_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int64_t ld, int box_heads,
-              int box_rows) {
-  static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      ptr = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }();
-  if (enc == nullptr) return false;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(ld) * 2};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool PAGED>
 int launch_tc(const AttendArgs& a, cudaStream_t s) {
   using C = SvCfg<D>;
@@ -742,13 +720,32 @@ int launch_tc(const AttendArgs& a, cudaStream_t s) {
       !rows_map(&mk, k, rows, a.hkv, D, a.ldk, 1, p.box_rows) ||
       !rows_map(&mv, v, rows, a.hkv, D, a.ldv, 1, p.box_rows))
     return PA_ERR_CUDA;
-  if (cudaFuncSetAttribute(attend_tc_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
-      cudaSuccess)
-    return PA_ERR_CUDA;
+  const int rc = allow_smem<attend_tc_kernel<D, PAGED>>(C::SMEM_BYTES);
+  if (rc != PA_OK) return rc;
   return launch_overlapped(attend_tc_kernel<D, PAGED>, dim3(tile_blocks(a) < kSms ? tile_blocks(a) : kSms), 384, C::SMEM_BYTES, s, mq, mk, mv, p);
 }
 
 }  // namespace
+
+bool rows_map(void* map, const void* base, int64_t rows, int heads, int d, int64_t ld, int box_heads,
+              int box_rows) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 int launch_attend_tc(const AttendArgs& a, cudaStream_t s) {
   if (a.block_table)
