@@ -21,10 +21,13 @@ constexpr int kBuckets = 256;
 // tiles.  Cutting keys is looked at while the rows give less than three waves
 // of blocks: from there on there is nothing to gain.
 constexpr int kPieceCost = 5;
+constexpr int kCuts = 32;
 constexpr int kMaxCut = 64;
 constexpr int kMaxCutItems = 1024;
-// K and V of this many bytes stay in L2 (126 MB) beside q and o.
-constexpr double kL2Keys = 64e6;
+// K and V of this many bytes stay in L2 (126 MB) beside q and o.  Pieces of
+// more, but of no more than two waves per head, are also taken over all heads
+// in order of depth: a balanced end is worth more than the reuse.
+constexpr double kL2Keys = 100e6;
 
 struct Lens {
   int64_t row0, q, kv;
@@ -74,7 +77,8 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
   __shared__ int hist[kBuckets];
   __shared__ int depth[kMaxCutItems], part_of[kMaxCutItems], first_piece[kMaxCutItems + 1];
   __shared__ int deepest, n_merge;
-  __shared__ unsigned long long best, keys;
+  __shared__ unsigned key_tiles;
+  __shared__ int cost_pieces[kCuts], cost_cuts[kCuts], cost_load[kCuts], best;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   if (tid < static_cast<int>(kStatusBytes / 4)) reinterpret_cast<int32_t*>(a.status)[tid] = 0;
   for (int c = tid; c < a.decode_ctas; c += threads) a.done[c] = 0;
@@ -84,14 +88,15 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     items[0] = 0;
     deepest = 0;
     n_merge = 0;
-    best = ~0ull;
-    keys = 0;
+    key_tiles = 0;
   }
+  if (tid < kCuts) cost_pieces[tid] = cost_cuts[tid] = cost_load[tid] = 0;
   __syncthreads();
   int64_t item_base = 0, unit_base = 0;
   for (int b0 = 0; b0 < a.B; b0 += threads) {
     const int b = b0 + tid;
     int64_t ni = 0, nu = 0;
+    int depth_b = 0;
     if (b < a.B) {
       const Lens r = lens_of(a, b, max_kv, true);
       if (r.q > 0) {
@@ -99,11 +104,17 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
           const int64_t groups = (r.kv + kPlanTile - 1) / kPlanTile;
           nu = (groups > 0 ? groups : 1) * a.hkv;
         } else {
-          ni = (r.q + a.tile_tokens - 1) / a.tile_tokens;
-          atomicMax(&deepest, static_cast<int>((keys_seen(r.kv, r.q, r.q) + kPlanTile - 1) / kPlanTile));
-          atomicAdd(&keys, static_cast<unsigned long long>(r.kv));
+          ni = (static_cast<uint32_t>(r.q) + a.tile_tokens - 1) / static_cast<uint32_t>(a.tile_tokens);
+          depth_b = static_cast<int>((r.kv + kPlanTile - 1) / kPlanTile);
         }
       }
+    }
+    depth_b = max(depth_b, 0);
+    const int warp_deepest = __reduce_max_sync(0xffffffffu, depth_b);
+    const unsigned warp_tiles = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(depth_b));
+    if (lane == 0 && warp_deepest > 0) {
+      atomicMax(&deepest, warp_deepest);
+      atomicAdd(&key_tiles, warp_tiles);
     }
     int64_t i_all, u_all;
     block_incl_scan2<int64_t>(ni, nu, tmp[(b0 / threads) & 1], &i_all, &u_all);
@@ -156,33 +167,38 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
       __syncthreads();
       // the number of cuts of the deepest rows that ends first: blocks run in
       // waves of one per slot, or, past one wave, fill the slots evenly with
-      // half a piece of slack; a cut adds the merge of its partial results
-      for (int s = warp + 1; s <= kMaxCut && s <= deepest; s += threads / 32) {
-        const int c = (deepest + s - 1) / s;
-        int np = 0, cuts = 0;
-        float load = 0.f;
-        for (int i = lane; i < n; i += 32) {
-          const int d = depth[i], p = d > c ? (d + c - 1) / c : 1;
-          np += p;
-          cuts += p > 1 ? p : 0;
-          load += static_cast<float>(d) + kPieceCost * p;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          np += __shfl_xor_sync(0xffffffffu, np, o);
-          cuts += __shfl_xor_sync(0xffffffffu, cuts, o);
-          load += __shfl_xor_sync(0xffffffffu, load, o);
-        }
-        if (lane == 0 && cuts <= a.part_cap) {
-          float cost = static_cast<float>(kPieceCost + c);
-          if (static_cast<int64_t>(np) * a.hkv > a.slots)
-            cost = fmaxf(cost, load * a.hkv / a.slots + 0.5f * (kPieceCost + c));
-          if (s > 1) cost += 3.f + s / 8.f;
-          atomicMin(&best, (static_cast<unsigned long long>(__float_as_uint(cost)) << 32) | s);
-        }
+      // half a piece of slack; a cut adds the merge of its partial results.
+      // One lane per number, the rows spread over the warps.
+      const int cuts = lane < 20 ? lane + 1 : min(kMaxCut, 20 + (lane - 19) * 4);   // 1 .. 20, then every fourth
+      const int c = (deepest + cuts - 1) / cuts;
+      int np = 0, nc = 0, load = 0;
+      const float inv = 1.f / c;
+      for (int i = warp; i < n; i += threads / 32) {
+        const int d = depth[i], x = d + c - 1;
+        int p = static_cast<int>(x * inv);   // x / c, put right by at most one
+        p += (p + 1) * c <= x;
+        p -= p * c > x;
+        p = max(p, 1);
+        np += p;
+        nc += p > 1 ? p : 0;
+        load += d + kPieceCost * p;
+      }
+      atomicAdd(&cost_pieces[lane], np);
+      atomicAdd(&cost_cuts[lane], nc);
+      atomicAdd(&cost_load[lane], load);
+      __syncthreads();
+      if (warp == 0) {
+        float cost = static_cast<float>(kPieceCost + c);
+        if (static_cast<int64_t>(cost_pieces[lane]) * a.hkv > a.slots)
+          cost = fmaxf(cost, static_cast<float>(cost_load[lane]) * a.hkv / a.slots + 0.5f * (kPieceCost + c));
+        if (cuts > 1) cost += 3.f + cuts / 8.f;
+        if (cost_cuts[lane] > a.part_cap || cuts > deepest) cost = INFINITY;
+        const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));
+        const unsigned who = __ballot_sync(0xffffffffu, __float_as_uint(cost) == least);
+        if (lane == __ffs(who) - 1) best = cuts;
       }
       __syncthreads();
-      if (best != ~0ull) parts = static_cast<int>(best & 0xffffffffu);
+      parts = best;
       cut = parts > 1;
     }
     if (cut) {
@@ -218,15 +234,34 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
       }
       if (tid == 0) first_piece[0] = 0;
       __syncthreads();
-      for (int x = tid; x < n_pieces; x += threads) {
-        const int i = upper_index(first_piece, n + 1, x);
+      // the longest first, by a counting sort (no piece is longer than `chunk`)
+      const bool sort = static_cast<int64_t>(n_pieces) * a.hkv > a.slots;
+      auto bucket = [&](int d) { return kBuckets - 1 - static_cast<int>(static_cast<int64_t>(d) * (kBuckets - 1) / chunk); };
+      auto piece_len = [&](int x, int& i, int& kt0) {
+        i = upper_index(first_piece, n + 1, x);
         const int p = first_piece[i + 1] - first_piece[i], k = x - first_piece[i];
-        const int b = upper_index(items, a.B + 1, i);
-        const Lens r = lens_of(a, b, max_kv, false);
         const int lo = depth[i] / p, more = depth[i] % p;   // the first `more` pieces have a tile more
-        const int kt0 = k * lo + min(k, more);
-        put_piece(a, x, b, r, (i - items[b]) * a.tile_tokens, kt0, kt0 + lo + (k < more),
-                  part_of[i] < 0 ? -1 : part_of[i] + k);
+        kt0 = k * lo + min(k, more);
+        return lo + (k < more);
+      };
+      if (sort) {
+        for (int x = tid; x < n_pieces; x += threads) {
+          int i, kt0;
+          atomicAdd(&hist[bucket(piece_len(x, i, kt0))], 1);
+        }
+        __syncthreads();
+        const int64_t h = tid < kBuckets ? hist[tid] : 0;
+        int64_t at = h, none = 0, all, none_all;
+        block_incl_scan2<int64_t>(at, none, tmp[1], &all, &none_all);
+        if (tid < kBuckets) hist[tid] = static_cast<int>(at - h);
+        __syncthreads();
+      }
+      for (int x = tid; x < n_pieces; x += threads) {
+        int i, kt0;
+        const int len = piece_len(x, i, kt0);
+        const int b = upper_index(items, a.B + 1, i);
+        put_piece(a, sort ? atomicAdd(&hist[bucket(len)], 1) : x, b, lens_of(a, b, max_kv, false),
+                  (i - items[b]) * a.tile_tokens, kt0, kt0 + len, part_of[i] < 0 ? -1 : part_of[i] + x - first_piece[i]);
       }
     } else {
       // deepest first: a counting sort by depth (the order inside a bucket is
@@ -264,51 +299,70 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     a.head->n_items = n_merge;
     a.head->abort = 0;
     a.head->next = 0;
-    a.head->heads_inner = static_cast<double>(keys) * a.hkv * a.d * (a.dtype == PA_BF16 ? 4 : 8) <= kL2Keys;
+    a.head->heads_inner = static_cast<double>(key_tiles) * kPlanTile * a.hkv * a.d * (a.dtype == PA_BF16 ? 4 : 8) <= kL2Keys ||
+                           n_pieces <= 2 * a.slots;
   }
 }
 
 // Rows cut into pieces: lse = ln sum_p exp(lse_p), o = sum_p exp(lse_p - lse) o_p,
-// in piece order.  One warp per row; the partial rows' loads are independent
-// and go out several at a time.
+// in piece order.  One warp per row, the rows of all items in one sequence.
+// Bound by the latency of its loads: the parts' lse are loaded together, and
+// eight of their rows at a time, the first eight without waiting for the
+// weights; the grid is one wave (a second one's start costs more than its work).
 template <typename OT, int D>
-__global__ void __launch_bounds__(256) attend_merge_kernel(AttendArgs a) {
-  constexpr int VPL = D / 32, U = 16 / VPL;   // elements of a lane, parts in flight
+__global__ void __launch_bounds__(256, 4) attend_merge_kernel(AttendArgs a) {
+  constexpr int VPL = D / 32, U = 8;   // elements of a lane, parts in flight (a divisor of 32)
   using Vec = std::conditional_t<VPL == 4, float4, float2>;
   grid_dep_wait();
-  if (static_cast<int>(blockIdx.x) >= a.head->n_items) return;
-  const MergeItem it = a.items[blockIdx.x];
-  const int kvh = blockIdx.y, g = a.hq / a.hkv;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = it.n_tok * g;
+  const int g = a.hq / a.hkv, lane = threadIdx.x & 31;
   const int64_t step = static_cast<int64_t>(a.hkv) * a.tile_rows;   // rows from one partial result to the next
-  const int64_t base = (static_cast<int64_t>(it.part0) * a.hkv + kvh) * a.tile_rows;
-  for (int r = blockIdx.z * 8 + warp; r < rows; r += gridDim.z * 8) {
-    const float* ls = a.part_lse + base + r;
-    const Vec* src = reinterpret_cast<const Vec*>(a.part_o + (base + r) * D) + lane;
+  const int64_t total = a.head->n_items * step;
+  for (int64_t x = blockIdx.x * 8 + (threadIdx.x >> 5); x < total; x += static_cast<int64_t>(gridDim.x) * 8) {
+    const int r = static_cast<int>(x % a.tile_rows);
+    const int64_t y = x / a.tile_rows;
+    const int kvh = static_cast<int>(y % a.hkv);
+    const MergeItem it = a.items[y / a.hkv];
+    if (r >= it.n_tok * g) continue;
+    const int64_t base = (static_cast<int64_t>(it.part0) * a.hkv + kvh) * a.tile_rows + r;
+    const float* ls = a.part_lse + base;
+    const Vec* src = reinterpret_cast<const Vec*>(a.part_o + base * D) + lane;
     float m = -INFINITY;
+#pragma unroll 1
     for (int p = lane; p < it.n_parts; p += 32) m = fmaxf(m, ls[p * step]);
+    float v[U][VPL];
+    auto load = [&](int k, int p) {
+      const Vec x = src[p * step * (D / VPL)];
+      v[k][0] = x.x;
+      v[k][1] = x.y;
+      if constexpr (VPL == 4) {
+        v[k][2] = x.z;
+        v[k][3] = x.w;
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (k < it.n_parts) load(k, k);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float sub = m == -INFINITY ? 0.f : m;   // a NaN stays one
-    float z = 0.f;
-    float acc[VPL] = {};
-    for (int p0 = 0; p0 < it.n_parts; p0 += 32) {
-      const float w = p0 + lane < it.n_parts ? expf(ls[(p0 + lane) * step] - sub) : 0.f;
-      z += w;
-      const int n = min(32, it.n_parts - p0);
-      for (int p = 0; p < n; p += U) {
-        Vec v[U];
+    float z = 0.f, w = 0.f, acc[VPL] = {};
+#pragma unroll 1
+    for (int p = 0; p < it.n_parts; p += U) {
+      if ((p & 31) == 0) {
+        w = p + lane < it.n_parts ? expf(ls[(p + lane) * step] - sub) : 0.f;
+        z += w;
+      }
+      if (p > 0) {
 #pragma unroll
         for (int k = 0; k < U; ++k)
-          if (p + k < n) v[k] = src[(p0 + p + k) * step * (D / VPL)];
+          if (p + k < it.n_parts) load(k, p + k);
+      }
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          const float wk = __shfl_sync(0xffffffffu, w, (p + k) & 31);
-          if (p + k >= n || wk == 0.f) continue;   // (a piece without a visible key)
-          const float* x = reinterpret_cast<const float*>(&v[k]);
+      for (int k = 0; k < U; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, (p + k) & 31);
+        if (p + k < it.n_parts && wk != 0.f) {   // (zero: a piece without a visible key)
 #pragma unroll
-          for (int e = 0; e < VPL; ++e) acc[e] += wk * x[e];
+          for (int i = 0; i < VPL; ++i) acc[i] += wk * v[k][i];
         }
       }
     }
@@ -326,19 +380,16 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(AttendArgs a) {
 
 template <typename OT>
 int merge(const AttendArgs& a, cudaStream_t s) {
-  // about eight waves of eight warps; a block takes several rows when there are more
-  const int most = (a.tile_rows + 7) / 8, fill = 8 * kSms / (a.item_cap * a.hkv) + 1;
-  const dim3 grid(a.item_cap, a.hkv, most < fill ? most : fill);
+  const int64_t rows = static_cast<int64_t>(a.item_cap) * a.hkv * a.tile_rows;
+  const int64_t want = (rows + 7) / 8;
+  const dim3 grid(static_cast<unsigned>(want < 4 * kSms ? want : 4 * kSms));
   return launch_overlapped(a.d == 128 ? attend_merge_kernel<OT, 128> : attend_merge_kernel<OT, 64>, grid, 256, 0, s, a);
 }
 
 }  // namespace
 
-// few requests and rows and nothing to cut: the fewer warps at its barriers, the
-// sooner it ends
-static int plan_threads(const AttendArgs& a) {
-  return a.B <= 256 && a.piece_cap <= 1024 && a.part_cap == 0 ? 256 : 1024;
-}
+// few requests and rows: the fewer warps at its barriers, the sooner it ends
+static int plan_threads(const AttendArgs& a) { return a.B <= 256 && a.piece_cap <= 1024 ? 256 : 1024; }
 
 size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws) {
   const int g = a.hq / a.hkv;

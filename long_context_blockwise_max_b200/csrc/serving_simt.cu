@@ -2,10 +2,14 @@
 // of fp32 inputs (every product and sum in fp32).
 //
 // Block = one piece: up to ROWS (token, query head) rows of one kv head
-// against its key tiles, 64 keys at a time through shared memory, 256
+// against its key tiles, 64 keys at a time through shared memory (16-byte
+// asynchronous copies, the next tile's under way during the current one), 256
 // threads as 16 x 16: a thread has ROWS / 16 rows x 4 keys of the scores and
 // the same rows x D / 16 columns of o.  Online softmax in log2 units, the
 // running maximum and sum of a row kept by the 16 threads that share it.
+// With 64 rows the fp32 FMAs and the shared-memory reads that feed them (12
+// to 16 per 64 FMAs) are about even; with 16 rows (few new tokens) the reads
+// bound it.
 #include "serving.h"
 
 namespace pa {
@@ -18,24 +22,30 @@ template <int D, int ROWS>
 struct SimtCfg {
   static constexpr int LDK = D + 4;              // 16 keys of a load fall on different banks
   static constexpr int LDP = kKeys + 4;
+  static constexpr int STAGE = kKeys * (LDK + D);   // K, then V
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + ROWS * D;
-  static constexpr int OFF_V = OFF_K + kKeys * LDK;
-  static constexpr int OFF_P = OFF_V + kKeys * D;
+  static constexpr int OFF_KV = OFF_Q + ROWS * D;
+  static constexpr int OFF_P = OFF_KV + 2 * STAGE;
   static constexpr int FLOATS = OFF_P + ROWS * LDP;
-  static constexpr int SMEM = FLOATS * 4 + kKeys * 8;
+  static constexpr int SMEM = FLOATS * 4 + 2 * kKeys * 8;
 };
 
-template <typename T, int D, int ROWS>
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool valid) {
+  const int n = valid ? 16 : 0;   // 0: fill the 16 bytes with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(n)
+               : "memory");
+}
+
+template <int D, int ROWS>
 __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
   using C = SimtCfg<D, ROWS>;
   constexpr int R = ROWS / 16, CV = D / 64;      // rows, float4 columns of a thread
   extern __shared__ __align__(16) float sm[];
   float* sq = sm + C::OFF_Q;
-  float* sk = sm + C::OFF_K;
-  float* sv = sm + C::OFF_V;
   float* sp = sm + C::OFF_P;
-  int64_t* slot = reinterpret_cast<int64_t*>(sm + C::FLOATS);
+  int64_t* slot = reinterpret_cast<int64_t*>(sm + C::FLOATS);   // [2][keys] rows of a tile's keys, -1: none
   grid_dep_wait();
   grid_dep_launch();
   int at, kvh;
@@ -46,18 +56,45 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int n_rows = min(a.tile_tokens, pc.q_len - pc.tok0) * g;
   const float scale = static_cast<float>(kLog2e / sqrt(static_cast<double>(D)));
-  const T* Q = static_cast<const T*>(a.q);
-  const T* K = static_cast<const T*>(a.k);
-  const T* V = static_cast<const T*>(a.v);
-  for (int e = tid; e < ROWS * D; e += 256) {
-    const int r = e / D, m = e % D;
-    float x = 0.f;
+  const float* Q = static_cast<const float*>(a.q);
+  const float* K = static_cast<const float*>(a.k) + kvh * D;
+  const float* V = static_cast<const float*>(a.v) + kvh * D;
+  const int64_t key_lo = static_cast<int64_t>(pc.kt0) * kPlanTile;
+  const int64_t key_hi = min(static_cast<int64_t>(pc.kt1) * kPlanTile,
+                             keys_seen(pc.kv_len, pc.q_len, min(pc.q_len, pc.tok0 + a.tile_tokens)));
+  // rows of the tile that starts at key c0, by the first threads
+  auto look_up = [&](int64_t c0, int s) {
+    if (tid < kKeys) {
+      const int64_t key = c0 + tid;
+      slot[s * kKeys + tid] = key >= key_hi ? -1 : a.block_table ? key_slot(a, pc.b, key) : pc.row0 + key;
+    }
+  };
+  auto fetch = [&](int s) {
+    float* k = sm + C::OFF_KV + s * C::STAGE;
+    float* v = k + kKeys * C::LDK;
+#pragma unroll
+    for (int e = tid; e < kKeys * (D / 4); e += 256) {
+      const int key = e / (D / 4), m = (e % (D / 4)) * 4;
+      const int64_t row = slot[s * kKeys + key];
+      const bool valid = row >= 0;
+      copy16(k + key * C::LDK + m, valid ? K + row * a.ldk + m : Q, valid);
+      copy16(v + key * D + m, valid ? V + row * a.ldv + m : Q, valid);
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+  look_up(key_lo, 0);
+  look_up(key_lo + kKeys, 1);
+  for (int e = tid; e < ROWS * (D / 4); e += 256) {
+    const int r = e / (D / 4), m = (e % (D / 4)) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < n_rows) {
       const int64_t row = static_cast<int64_t>(pc.row0) + pc.tok0 + r / g;
-      x = to_f32(Q[row * a.ldq + (kvh * g + r % g) * D + m]);
+      x = *reinterpret_cast<const float4*>(Q + row * a.ldq + (kvh * g + r % g) * D + m);
     }
-    sq[e] = x;
+    *reinterpret_cast<float4*>(sq + r * D + m) = x;
   }
+  __syncthreads();
+  fetch(0);
   int64_t lim[R];                                // last visible key of each row
   float m_run[R], l_run[R], acc[R][4 * CV];
 #pragma unroll
@@ -70,31 +107,16 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
     for (int j = 0; j < 4 * CV; ++j) acc[i][j] = 0.f;
   }
   const int64_t lim_first = static_cast<int64_t>(pc.kv_len) - pc.q_len + pc.tok0;
-  const int64_t k1 = min(static_cast<int64_t>(pc.kt1) * kPlanTile,
-                         keys_seen(pc.kv_len, pc.q_len, min(pc.q_len, pc.tok0 + a.tile_tokens)));
-  for (int64_t c0 = static_cast<int64_t>(pc.kt0) * kPlanTile; c0 < k1; c0 += kKeys) {
+  int st = 0;
+  for (int64_t c0 = key_lo; c0 < key_hi; c0 += kKeys, st ^= 1) {
+    // the next tile into the other stage (its last reader passed the barrier
+    // at the end of the round before)
+    fetch(st ^ 1);
+    asm volatile("cp.async.wait_group 1;\n" ::: "memory");
     __syncthreads();
-    if (tid < kKeys) {
-      const int64_t key = c0 + tid;
-      int64_t at = -1;
-      if (key < k1) at = a.block_table ? key_slot(a, pc.b, key) : pc.row0 + key;
-      slot[tid] = at;
-    }
-    __syncthreads();
-    for (int e = tid; e < kKeys * (D / 4); e += 256) {
-      const int key = e / (D / 4), m = (e % (D / 4)) * 4;
-      const int64_t at = slot[key];
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (at >= 0) {
-        const T* ks = K + at * a.ldk + kvh * D + m;
-        const T* vs = V + at * a.ldv + kvh * D + m;
-        x = make_float4(to_f32(ks[0]), to_f32(ks[1]), to_f32(ks[2]), to_f32(ks[3]));
-        y = make_float4(to_f32(vs[0]), to_f32(vs[1]), to_f32(vs[2]), to_f32(vs[3]));
-      }
-      *reinterpret_cast<float4*>(sk + key * C::LDK + m) = x;
-      *reinterpret_cast<float4*>(sv + key * D + m) = y;
-    }
-    __syncthreads();
+    look_up(c0 + 2 * kKeys, st);
+    const float* sk = sm + C::OFF_KV + st * C::STAGE;
+    const float* sv = sk + kKeys * C::LDK;
     // scores of rows ty * R + i and keys tx + 16 * j
     float s[R][4];
 #pragma unroll
@@ -116,12 +138,14 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
           s[i][j] = fmaf(q4[i].w, k4[j].w, s[i][j]);
         }
     }
+    // (before the stores below: a tile that every row sees in full needs no mask)
+    const bool whole = c0 + kKeys - 1 <= lim_first;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       float mt = m_run[i];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = c0 + tx + 16 * j <= lim[i] ? s[i][j] * scale : -INFINITY;
+        s[i][j] = whole || c0 + tx + 16 * j <= lim[i] ? s[i][j] * scale : -INFINITY;
         mt = fmaxf(mt, s[i][j]);
       }
 #pragma unroll
@@ -143,28 +167,50 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
       for (int j = 0; j < 4 * CV; ++j) acc[i][j] *= alpha;
     }
     __syncwarp();   // a row's 16 threads are in one warp
-    // a tile that some row does not see in full: there a masked key must add
-    // nothing even if its V is not finite, so its product is skipped
-    const bool whole = c0 + kKeys - 1 <= lim_first;
-#pragma unroll 4
-    for (int key = 0; key < kKeys; ++key) {
-      float p[R];
-#pragma unroll
-      for (int i = 0; i < R; ++i) p[i] = sp[(ty * R + i) * C::LDP + key];
-#pragma unroll
-      for (int j = 0; j < CV; ++j) {
-        const float4 v4 = *reinterpret_cast<const float4*>(sv + key * D + 64 * j + 4 * tx);
+    if (whole) {
+#pragma unroll 2
+      for (int key = 0; key < kKeys; key += 4) {
+        float p[R][4];
 #pragma unroll
         for (int i = 0; i < R; ++i)
-          if (whole || c0 + key <= lim[i]) {
-            acc[i][4 * j] = fmaf(p[i], v4.x, acc[i][4 * j]);
-            acc[i][4 * j + 1] = fmaf(p[i], v4.y, acc[i][4 * j + 1]);
-            acc[i][4 * j + 2] = fmaf(p[i], v4.z, acc[i][4 * j + 2]);
-            acc[i][4 * j + 3] = fmaf(p[i], v4.w, acc[i][4 * j + 3]);
+          *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(sp + (ty * R + i) * C::LDP + key);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < CV; ++j) {
+            const float4 v4 = *reinterpret_cast<const float4*>(sv + (key + k) * D + 64 * j + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              acc[i][4 * j] = fmaf(p[i][k], v4.x, acc[i][4 * j]);
+              acc[i][4 * j + 1] = fmaf(p[i][k], v4.y, acc[i][4 * j + 1]);
+              acc[i][4 * j + 2] = fmaf(p[i][k], v4.z, acc[i][4 * j + 2]);
+              acc[i][4 * j + 3] = fmaf(p[i][k], v4.w, acc[i][4 * j + 3]);
+            }
           }
       }
+    } else {
+      // some row does not see some key: there a masked key must add nothing
+      // even if its V is not finite, so its product is skipped
+#pragma unroll 1
+      for (int key = 0; key < kKeys; ++key) {
+#pragma unroll
+        for (int j = 0; j < CV; ++j) {
+          const float4 v4 = *reinterpret_cast<const float4*>(sv + key * D + 64 * j + 4 * tx);
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+            if (c0 + key <= lim[i]) {
+              const float p = sp[(ty * R + i) * C::LDP + key];
+              acc[i][4 * j] = fmaf(p, v4.x, acc[i][4 * j]);
+              acc[i][4 * j + 1] = fmaf(p, v4.y, acc[i][4 * j + 1]);
+              acc[i][4 * j + 2] = fmaf(p, v4.z, acc[i][4 * j + 2]);
+              acc[i][4 * j + 3] = fmaf(p, v4.w, acc[i][4 * j + 3]);
+            }
+        }
+      }
     }
+    __syncthreads();   // the stage and its slots are refilled
   }
+  asm volatile("cp.async.wait_group 0;\n" ::: "memory");
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int r = ty * R + i;
@@ -172,37 +218,26 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
     const bool empty = l_run[i] == 0.f;   // no visible key
     const float inv = empty ? 0.f : 1.f / l_run[i];
     const float lse = empty ? -INFINITY : (m_run[i] + log2f(l_run[i])) * kLn2f;
-    if (pc.part >= 0) {
-      const int64_t at = (static_cast<int64_t>(pc.part) * a.hkv + kvh) * a.tile_rows + r;
+    const int64_t part = (static_cast<int64_t>(pc.part) * a.hkv + kvh) * a.tile_rows + r;
+    const int64_t row = (static_cast<int64_t>(pc.row0) + pc.tok0 + r / g) * a.hq + kvh * g + r % g;
+    float* dst = pc.part >= 0 ? a.part_o + part * D : static_cast<float*>(a.o) + row * D;
 #pragma unroll
-      for (int j = 0; j < CV; ++j)
-        *reinterpret_cast<float4*>(a.part_o + at * D + 64 * j + 4 * tx) =
-            make_float4(acc[i][4 * j] * inv, acc[i][4 * j + 1] * inv, acc[i][4 * j + 2] * inv, acc[i][4 * j + 3] * inv);
-      if (tx == 0) a.part_lse[at] = lse;
-    } else {
-      const int64_t at = (static_cast<int64_t>(pc.row0) + pc.tok0 + r / g) * a.hq + kvh * g + r % g;
-      T* dst = static_cast<T*>(a.o) + at * D;
-#pragma unroll
-      for (int j = 0; j < CV; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dst[64 * j + 4 * tx + e] = from_f32<T>(acc[i][4 * j + e] * inv);
-      if (tx == 0 && a.lse) a.lse[at] = lse;
+    for (int j = 0; j < CV; ++j)
+      *reinterpret_cast<float4*>(dst + 64 * j + 4 * tx) =
+          make_float4(acc[i][4 * j] * inv, acc[i][4 * j + 1] * inv, acc[i][4 * j + 2] * inv, acc[i][4 * j + 3] * inv);
+    if (tx == 0) {
+      if (pc.part >= 0) a.part_lse[part] = lse;
+      else if (a.lse) a.lse[row] = lse;
     }
   }
 }
 
-template <typename T, int D, int ROWS>
+template <int D, int ROWS>
 int launch(const AttendArgs& a, cudaStream_t s) {
   constexpr int smem = SimtCfg<D, ROWS>::SMEM;
-  const int rc = allow_smem<attend_simt_kernel<T, D, ROWS>>(smem);
+  const int rc = allow_smem<attend_simt_kernel<D, ROWS>>(smem);
   if (rc != PA_OK) return rc;
-  return launch_overlapped(attend_simt_kernel<T, D, ROWS>, dim3(tile_blocks(a)), 256, smem, s, a);
-}
-
-template <typename T>
-int launch_t(const AttendArgs& a, cudaStream_t s) {
-  if (a.tile_rows == 16) return a.d == 128 ? launch<T, 128, 16>(a, s) : launch<T, 64, 16>(a, s);
-  return a.d == 128 ? launch<T, 128, 64>(a, s) : launch<T, 64, 64>(a, s);
+  return launch_overlapped(attend_simt_kernel<D, ROWS>, dim3(tile_blocks(a)), 256, smem, s, a);
 }
 
 }  // namespace
@@ -215,6 +250,9 @@ int simt_blocks_per_sm(const AttendArgs& a) {
   return n < 2 ? n : 2;
 }
 
-int launch_attend_simt(const AttendArgs& a, cudaStream_t s) { return launch_t<float>(a, s); }
+int launch_attend_simt(const AttendArgs& a, cudaStream_t s) {
+  if (a.tile_rows == 16) return a.d == 128 ? launch<128, 16>(a, s) : launch<64, 16>(a, s);
+  return a.d == 128 ? launch<128, 64>(a, s) : launch<64, 64>(a, s);
+}
 
 }  // namespace pa

@@ -277,9 +277,6 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->work_full[k & 1]);
       if (!get_item(bars, tpt, k, it)) break;
-      if (lane == 0) unit = gridDim.x + atomicAdd(&a.head->next, 1u);
-      unit = __shfl_sync(0xffffffffu, unit, 0);
-      fetch();
       const Piece& pc = it.pc;
       // row coordinate of this lane's box of tile j
       auto row_of = [&](int j) -> int {
@@ -327,6 +324,10 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
         n_g1 += guarded && st == 1;
         row = next;
       }
+      // (not before: a unit taken early would wait here while other blocks run out of work)
+      if (lane == 0) unit = gridDim.x + atomicAdd(&a.head->next, 1u);
+      unit = __shfl_sync(0xffffffffu, unit, 0);
+      fetch();
     }
     if (lane == 0) {
       if (!ok) fail(1);

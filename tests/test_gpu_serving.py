@@ -306,6 +306,16 @@ def test_paged_heads(S, dtype, d, hq, hkv, case):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("q_lens,kv_lens,hkv", [([64], [30000], 1), ([40, 1], [9000, 12000], 2), ([2], [70000], 1)])
+def test_paged_keys_cut_into_many_pieces(S, dtype, q_lens, kv_lens, hkv):
+    # few rows over long caches: more than 32 partial results per row
+    c = paged_batch(q_lens, kv_lens, 4 * hkv, hkv, 64, 64, DTYPES[dtype], seed=8)
+    o, lse, ws = S.pa_paged_attend(c["q"], c["cu_q"], c["kv_len"], c["table"], c["k_pages"], c["v_pages"], c["max_q"])
+    assert ok(S, ws) == 0
+    check_paged(c, o, lse, "many pieces")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("q_lens,kv_lens", [([3, 1, 5], [1, 0, 5]), ([40, 130], [3, 100]), ([1], [0])])
 def test_paged_rows_that_see_nothing(S, dtype, q_lens, kv_lens):
     c = paged_batch(q_lens, kv_lens, 8, 2, 64, 16, DTYPES[dtype], seed=9)
