@@ -85,8 +85,9 @@ struct SvBars {
   unsigned long long first[2][3][128];
   float ml[2][2][2][128]; // [in turn][warpgroup][maximum, sum][row]
   struct {
-    int4 piece[2];        // a Piece
-    int kvh;              // its kv head; -1: no more
+    int4 rows;            // row0, tok0, q_len, kv_len
+    int4 keys;            // kt0, n, part, kvh (-1: no more)
+    int4 tiles;           // nt0, nt1, g0, 2 * request + two
   } work[2];
 };
 static_assert(sizeof(SvBars) + 1024 <= 13 * 1024, "barriers and alignment slack");
@@ -145,35 +146,34 @@ __device__ void guard_tile(uint8_t* v, int first_row, int n_keys, int key0, int 
 
 // A piece as its roles see it.
 struct Item {
-  Piece pc;
-  int kvh;
-  int ctx;        // position of the first new token (may be negative)
-  int n;          // key tiles
-  bool two;       // two row tiles
-  int nt0, nt1;   // key tiles of each warpgroup: with two row tiles those up to its
-                  // last row's limit, of all; with one, every other
-  int g0;         // first guarded tile: tiles from it on hold a key that the first row does not see
+  int row0, tok0, q_len, kv_len;   // as in Piece
+  int kt0, n;                      // first key tile, key tiles
+  int part, kvh;
+  int nt0, nt1;                    // key tiles of each warpgroup: with two row tiles those up to
+                                   // its last row's limit, of all; with one, every other
+  int g0;                          // first guarded tile: those from it on hold a key that the first row does not see
+  bool two;                        // two row tiles
+  int b;                           // request
+  int ctx;                         // position of the first new token (may be negative)
 };
 
 // The k-th piece of this block, once it is there; false: no more.
-__device__ __forceinline__ bool get_item(const SvBars* bars, int tpt, int k, Item& it) {
-  const int4 x = bars->work[k & 1].piece[0], y = bars->work[k & 1].piece[1];
-  it.kvh = bars->work[k & 1].kvh;
-  it.pc = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-  const Piece& pc = it.pc;
-  it.ctx = pc.kv_len - pc.q_len;
-  it.n = pc.kt1 - pc.kt0;
-  it.two = pc.tok0 + tpt < pc.q_len;
-  if (it.two) {
-    const int seen = max(0, it.ctx + pc.tok0 + tpt);    // keys that tile 0 sees (it is full)
-    it.nt0 = max(0, min(it.n, (seen + kKeyTile - 1) / kKeyTile - pc.kt0));
-    it.nt1 = it.n;
-  } else {
-    it.nt0 = (it.n + 1) / 2;
-    it.nt1 = it.n / 2;
-  }
-  it.g0 = max(0, max(0, it.ctx + pc.tok0 + 1) / kKeyTile - pc.kt0);
+__device__ __forceinline__ bool get_item(const SvBars* bars, int k, Item& it) {
+  const int4 x = bars->work[k & 1].rows, y = bars->work[k & 1].keys, z = bars->work[k & 1].tiles;
+  it = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, (z.w & 1) != 0, z.w >> 1, x.w - x.z};
   return it.kvh >= 0;
+}
+
+// Puts piece `pc` (kv head -1: the end) where get_item finds it.
+__device__ __forceinline__ void put_item(SvBars* bars, int k, int tpt, const Piece& pc, int kvh) {
+  const int ctx = pc.kv_len - pc.q_len, n = pc.kt1 - pc.kt0;
+  const bool two = pc.tok0 + tpt < pc.q_len;
+  const int seen = max(0, ctx + pc.tok0 + tpt);    // keys that tile 0 sees (it is full)
+  const int nt0 = two ? max(0, min(n, (seen + kKeyTile - 1) / kKeyTile - pc.kt0)) : (n + 1) / 2;
+  bars->work[k & 1].rows = make_int4(pc.row0, pc.tok0, pc.q_len, pc.kv_len);
+  bars->work[k & 1].keys = make_int4(pc.kt0, n, pc.part, kvh);
+  bars->work[k & 1].tiles = make_int4(nt0, two ? n : n / 2, max(0, max(0, ctx + pc.tok0 + 1) / kKeyTile - pc.kt0),
+                                         2 * pc.b + two);
 }
 
 template <int D, bool PAGED>
@@ -200,13 +200,13 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       mbar_init(&bars->v_full[s], 1);
       mbar_init(&bars->v_empty[s], 1);
       mbar_init(&bars->vg_full[s], 1);
-      mbar_init(&bars->v_ready[s], 64);
+      mbar_init(&bars->v_ready[s], 2);
       mbar_init(&bars->s_full[s], 1);
-      mbar_init(&bars->p_full[s], 128);
+      mbar_init(&bars->p_full[s], 4);
       mbar_init(&bars->o_final[s], 1);
-      mbar_init(&bars->noted[s], 64);
-      mbar_init(&bars->done[s], 256);
-      mbar_init(&bars->ml_full[s], 128);
+      mbar_init(&bars->noted[s], 2);
+      mbar_init(&bars->done[s], 8);
+      mbar_init(&bars->ml_full[s], 4);
       mbar_init(&bars->work_full[s], 1);
       bars->odd[s] = 0;
     }
@@ -253,17 +253,17 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
     uint32_t n_q = 0, n_k = 0;          // copies issued: Q's and K tiles,
     uint32_t n_v0 = 0, n_v1 = 0, n_g0 = 0, n_g1 = 0;   // V tiles of each stage, guarded ones
     // Units of work: this block's first, then whichever comes next over all
-    // blocks (the deepest come first, so the blocks end together).  Lane l of
-    // the first two holds the l-th half of the piece after the current one.
+    // blocks (the deepest come first, so the blocks end together).
     const unsigned total = static_cast<unsigned>(a.head->n_pieces) * static_cast<unsigned>(a.hkv);
     unsigned unit = blockIdx.x;
     int at = 0, kvh = -1;
-    int4 half = make_int4(0, 0, 0, 0);
+    Piece after = {};                   // the piece after the current one
     auto fetch = [&]() {
       kvh = -1;
       if (unit < total) {
         piece_at(a, unit, &at, &kvh);
-        if (lane < 2) half = reinterpret_cast<const int4*>(a.pieces + at)[lane];
+        const int4 x = reinterpret_cast<const int4*>(a.pieces + at)[0], y = reinterpret_cast<const int4*>(a.pieces + at)[1];
+        after = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
       }
     };
     fetch();
@@ -272,21 +272,21 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
     for (int k = 0; ok; ++k) {
       // the slot's previous piece (two before) is finished
       if (k >= 2 && !wait(&bars->done[k & 1], (k >> 1) - 1)) { ok = false; break; }
-      if (lane < 2) bars->work[k & 1].piece[lane] = half;
-      if (lane == 2) bars->work[k & 1].kvh = kvh;
+      if (lane == 0) {
+        put_item(bars, k, tpt, after, kvh);
+        mbar_arrive(&bars->work_full[k & 1]);
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->work_full[k & 1]);
-      if (!get_item(bars, tpt, k, it)) break;
-      const Piece& pc = it.pc;
+      if (!get_item(bars, k, it)) break;
       // row coordinate of this lane's box of tile j
       auto row_of = [&](int j) -> int {
-        if (!PAGED) return pc.row0 + j * kKeyTile;
+        if (!PAGED) return it.row0 + j * kKeyTile;
         const int64_t key = static_cast<int64_t>(j) * kKeyTile + lane * p.box_rows;
-        if (lane >= nbox || key >= pc.kv_len) return p.oob_row;
-        const int64_t slot = key_slot(a, pc.b, key);
+        if (lane >= nbox || key >= it.kv_len) return p.oob_row;
+        const int64_t slot = key_slot(a, it.b, key);
         return slot < 0 ? p.oob_row : static_cast<int>(slot);
       };
-      int row = it.n > 0 ? row_of(pc.kt0) : 0;
+      int row = it.n > 0 ? row_of(it.kt0) : 0;
       if (k > 0 && !wait(&bars->q_empty, k - 1)) { ok = false; break; }
       if (lane == 0) {
         const int qt = it.two ? 2 : 1;
@@ -294,13 +294,13 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
         for (int t = 0; t < qt; ++t)
           for (int kb = 0; kb < C::NKB; ++kb)
             tma_load_3d(sQ + t * C::TILE_BYTES + kb * C::KB_BYTES, &tmQ, &bars->q_full, kb * 64, it.kvh * g,
-                        pc.row0 + pc.tok0 + t * tpt);
+                        it.row0 + it.tok0 + t * tpt);
       }
       ++n_q;
       for (int jj = 0; jj < it.n; ++jj, ++tile) {
         const int st = tile & 1;
         const uint32_t ph = tile >> 1;
-        const int next = jj + 1 < it.n ? row_of(pc.kt0 + jj + 1) : 0;
+        const int next = jj + 1 < it.n ? row_of(it.kt0 + jj + 1) : 0;
         if (!wait(&bars->k_empty[st], ph + 1)) { ok = false; break; }
         if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], C::TILE_BYTES);
         __syncwarp();
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       Item it;
       for (int k = 0; ok; ++k, tile += it.n) {
         if (!wait_one(&bars->work_full[k & 1], k >> 1)) { fail(2); break; }
-        if (!get_item(bars, tpt, k, it)) break;
+        if (!get_item(bars, k, it)) break;
         const int n = it.n;
         auto wait_v = [&](int jj) {
           const int st = (tile + jj) & 1;
@@ -467,18 +467,20 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
     for (int k = 0; ok; ++k, tile += it.n) {
       // (a piece is there only when the one two before, whose notes it takes over, is finished)
       if (!wait(&bars->work_full[k & 1], k >> 1)) { ok = false; break; }
-      if (!get_item(bars, tpt, k, it)) break;
-      const int lim_first = it.ctx + it.pc.tok0;
+      if (!get_item(bars, k, it)) break;
+      const int lim_first = it.ctx + it.tok0;
       for (int jj = it.g0; jj < it.n; ++jj) {
         const int st = (tile + jj) & 1;
         if (!wait(&bars->vg_full[st], ph_g >> st)) { ok = false; break; }
         ph_g ^= 1u << st;
-        const int key0 = (it.pc.kt0 + jj) * kKeyTile;
-        guard_tile<D>(sV + st * C::TILE_BYTES, max(0, lim_first + 1 - key0), it.pc.kv_len - key0, key0, k, bars, tid);
+        const int key0 = (it.kt0 + jj) * kKeyTile;
+        guard_tile<D>(sV + st * C::TILE_BYTES, max(0, lim_first + 1 - key0), it.kv_len - key0, key0, k, bars, tid);
         fence_async_smem();
-        mbar_arrive(&bars->v_ready[st]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->v_ready[st]);
       }
-      mbar_arrive(&bars->noted[k & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->noted[k & 1]);
     }
     if (!ok && lane == 0) fail(11);
   } else {
@@ -501,13 +503,13 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       {
         if (!wait(&bars->work_full[k & 1], k >> 1)) { ok = false; break; }
         Item it;
-        if (!get_item(bars, tpt, k, it)) break;
-        const int tok_t = it.pc.tok0 + (it.two ? t * tpt : 0);   // first token of this warpgroup's rows
-        const bool valid = rl < tpt * g && tok_t + rt < it.pc.q_len;
-        lim = valid ? it.ctx + tok_t + rt : it.pc.kv_len - 1;                         // last visible key
+        if (!get_item(bars, k, it)) break;
+        const int tok_t = it.tok0 + (it.two ? t * tpt : 0);   // first token of this warpgroup's rows
+        const bool valid = rl < tpt * g && tok_t + rt < it.q_len;
+        lim = valid ? it.ctx + tok_t + rt : it.kv_len - 1;                         // last visible key
         lim_w = it.ctx + tok_t + static_cast<int>((sub * 32 * ginv) >> 16);           // the smallest of this warp's rows
         my = t == 0 ? it.nt0 : it.nt1;
-        key_first = (it.pc.kt0 + (it.two ? 0 : t)) * kKeyTile;
+        key_first = (it.kt0 + (it.two ? 0 : t)) * kKeyTile;
         key_step = it.two ? kKeyTile : 2 * kKeyTile;
       }
       float m_run = -INFINITY, l_run = 0.f;
@@ -579,25 +581,26 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&bars->p_full[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[t]);
       }
       if (!ok) break;
       // ---- the piece's output: its own O (two row tiles), or half of the
       // columns of both O's joined (one)
       if (!wait(&bars->noted[k & 1], k >> 1)) { ok = false; break; }
       Item it;
-      get_item(bars, tpt, k, it);
-      const Piece& pc = it.pc;
+      get_item(bars, k, it);
       const bool two = it.two;
-      const int tok_t = pc.tok0 + (two ? t * tpt : 0);
-      const bool valid = rl < tpt * g && tok_t + rt < pc.q_len;
+      const int tok_t = it.tok0 + (two ? t * tpt : 0);
+      const bool valid = rl < tpt * g && tok_t + rt < it.q_len;
       const int n_other = t == 0 ? it.nt1 : it.nt0;
       float w_own = 1.f, w_oth = 0.f;
       if (!two) {
         float (*ml)[2][128] = bars->ml[n_ml & 1];
         ml[t][0][rl] = m_run;
         ml[t][1][rl] = l_run;
-        mbar_arrive(&bars->ml_full[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->ml_full[t]);
         if (!wait(&bars->ml_full[t ^ 1], n_ml++)) { ok = false; break; }
         const float m2 = ml[t ^ 1][0][rl], l2 = ml[t ^ 1][1][rl];
         const float m = fmaxf(m_run, m2);
@@ -619,13 +622,13 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       w_own *= inv;
       w_oth *= inv;
       const bool odd = *reinterpret_cast<volatile int*>(&bars->odd[k & 1]) == k + 1;
-      const int64_t prow = (static_cast<int64_t>(pc.part) * a.hkv + it.kvh) * a.tile_rows + (two ? t * tpt * g : 0) + rl;
-      const int rows = min(tpt, pc.q_len - tok_t) * g;     // rows of this tile
+      const int64_t prow = (static_cast<int64_t>(it.part) * a.hkv + it.kvh) * a.tile_rows + (two ? t * tpt * g : 0) + rl;
+      const int rows = min(tpt, it.q_len - tok_t) * g;     // rows of this tile
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) +
-                           ((static_cast<int64_t>(pc.row0) + tok_t) * a.hq + it.kvh * g) * D;
+                           ((static_cast<int64_t>(it.row0) + tok_t) * a.hq + it.kvh * g) * D;
       if (valid && (two || t == 0)) {
-        if (pc.part >= 0) a.part_lse[prow] = lse;
-        else if (a.lse) a.lse[(static_cast<int64_t>(pc.row0) + tok_t + rt) * a.hq + it.kvh * g + rh] = lse;
+        if (it.part >= 0) a.part_lse[prow] = lse;
+        else if (a.lse) a.lse[(static_cast<int64_t>(it.row0) + tok_t + rt) * a.hq + it.kvh * g + rh] = lse;
       }
       // 32 columns at a time; with one row tile each warpgroup writes half of them
       const int c_lo = two ? 0 : t * (D / 2), c_hi = two ? D : c_lo + D / 2;
@@ -638,14 +641,14 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
         if (my > 0) {
           tmem_ld_x32(o_tmem + c, ov);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = empty ? 0.f : __uint_as_float(ov[e]) * w_own;
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(ov[e]) * w_own;
         }
         if (!two && n_other > 0) {
           tmem_ld_x32(o_oth + c, ov);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] += empty ? 0.f : __uint_as_float(ov[e]) * w_oth;
+          for (int e = 0; e < 32; ++e) v[e] += __uint_as_float(ov[e]) * w_oth;
         }
-        if (pc.part >= 0) {
+        if (it.part >= 0) {
           if (valid) {
             float4* d4 = reinterpret_cast<float4*>(a.part_o + prow * D + c);
 #pragma unroll
@@ -682,7 +685,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
           const bool pos = seen(0, c), neg = seen(1, c), nan = seen(2, c) || (pos && neg);
           if (!pos && !neg && !nan) continue;
           const float add = nan ? __int_as_float(0x7fc00000) : pos ? INFINITY : -INFINITY;
-          if (pc.part >= 0) {
+          if (it.part >= 0) {
             a.part_o[prow * D + c] += add;
           } else {
             __nv_bfloat16* x = out + (static_cast<int64_t>(rt) * a.hq + rh) * D + c;
@@ -691,7 +694,8 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
         }
       }
       tc_fence_before();
-      mbar_arrive(&bars->done[k & 1]);   // O and the notes have been read
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->done[k & 1]);   // O and the notes have been read
     }
     if (!ok) fail(9);
   }
