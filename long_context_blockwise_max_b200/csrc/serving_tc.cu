@@ -110,6 +110,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+// An arrival that orders no memory (the caller's global stores need not be
+// done first); what it hands over is ordered by tcgen05 fences.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ bool bf16_nonfinite(uint32_t two) {
   return (two & 0x7f80u) == 0x7f80u || (two & 0x7f800000u) == 0x7f800000u;
 }
@@ -695,7 +700,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->done[k & 1]);   // O and the notes have been read
+      if (lane == 0) mbar_arrive_relaxed(&bars->done[k & 1]);   // O and the notes have been read
     }
     if (!ok) fail(9);
   }
