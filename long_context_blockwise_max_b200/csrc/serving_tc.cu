@@ -250,6 +250,226 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
   // the same for a whole warp, one answer for all lanes
   auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; };
 
+  // Registers from the first four warps to the softmax: 128 x 128 + 256 x 184 =
+  // 63488 of the 384 x 168 = 64512 that the block was launched with.
+  if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    // -------------------------------------------------------------- softmax
+    const int t = warp >= 8 ? 1 : 0;
+    const int sub = warp & 3;
+    const int rl = sub * 32 + lane;
+    const uint32_t ginv = 65536u / g + 1;            // row / g for rows below 128, g <= 64: exact
+    const int rt = static_cast<int>((rl * ginv) >> 16), rh = rl - rt * g;   // token and head of this thread's row
+    const uint32_t s_tmem = tmem + (static_cast<uint32_t>(sub * 32) << 16) + t * 256;
+    const uint32_t o_tmem = s_tmem + 128;
+    const uint32_t o_oth = tmem + (static_cast<uint32_t>(sub * 32) << 16) + (t ^ 1) * 256 + 128;
+    const uint64_t sc2 = f2_pack(C::SCALE, C::SCALE);
+    uint8_t* stage = smem + C::OFF_OUT + (warp - 4) * 2048;
+    uint32_t n_s = 0, n_own = 0, n_oth = 0, n_ml = 0;   // phases: scores, both final O's, exchanged maxima
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      // (read again for the output, so that little of it is held in registers beside the scores)
+      int my, lim, lim_w, key_first, key_step;
+      {
+        if (!wait(&bars->work_full[k & 1], k >> 1)) { ok = false; break; }
+        Item it;
+        if (!get_item(bars, k, it)) break;
+        const int tok_t = it.tok0 + (it.two ? t * tpt : 0);   // first token of this warpgroup's rows
+        const bool valid = rl < tpt * g && tok_t + rt < it.q_len;
+        lim = valid ? it.ctx + tok_t + rt : it.kv_len - 1;                         // last visible key
+        lim_w = it.ctx + tok_t + static_cast<int>((sub * 32 * ginv) >> 16);           // the smallest of this warp's rows
+        my = t == 0 ? it.nt0 : it.nt1;
+        key_first = (it.kt0 + (it.two ? 0 : t)) * kKeyTile;
+        key_step = it.two ? kKeyTile : 2 * kKeyTile;
+      }
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int i = 0; i < my; ++i) {
+        const int key0 = key_first + i * key_step;
+        if (!wait(&bars->s_full[t], n_s++)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t sr[128];
+        tmem_ld_x128(s_tmem, sr);
+        if (key0 + kKeyTile - 1 > lim_w) {
+          const int rel = lim - key0;                      // columns <= rel are visible
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if (e > rel) sr[e] = __float_as_uint(-INFINITY);
+        }
+        float mx[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx[e] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          mx[e & 7] = fmax3(mx[e & 7], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+        const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
+        const float m_new = fmaxf(m_run, mt);
+        const bool need = (m_new - m_run) * C::SCALE > 8.f;   // lazy rescale: only when P could exceed 2^8
+        float alpha = 1.f;
+        if (need) {
+          alpha = fast_exp2((m_run - m_new) * C::SCALE);
+          m_run = m_new;
+        }
+        const float m_use = (m_run == -INFINITY) ? 0.f : m_run * C::SCALE;
+        const uint64_t nm2 = f2_pack(-m_use, -m_use);
+        uint64_t acc2[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc2[e] = 0ull;   // two 0.0f
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1, p0, p1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])),
+                             sc2, nm2), x0, x1);
+            p0 = fast_exp2(x0);
+            p1 = fast_exp2(x1);
+            acc2[e & 3] = f2_add(acc2[e & 3], f2_pack(p0, p1));
+            pk[e] = pack2(p0, p1);
+          }
+          tmem_st_x16(s_tmem + 16 * c, pk);
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float a0, a1;
+          f2_unpack(acc2[e], a0, a1);
+          sum += a0 + a1;
+        }
+        l_run = l_run * alpha + sum;
+        if (i > 0 && __any_sync(0xffffffffu, need)) {
+          // O was last written by the previous PV, which completed before this
+          // S (the commit signalling S covers every earlier MMA).
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tmem_ld_x32(o_tmem + 32 * c, ov);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+            tmem_st_x32(o_tmem + 32 * c, ov);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[t]);
+      }
+      if (!ok) break;
+      // ---- the piece's output: its own O (two row tiles), or half of the
+      // columns of both O's joined (one)
+      if (!wait(&bars->noted[k & 1], k >> 1)) { ok = false; break; }
+      Item it;
+      get_item(bars, k, it);
+      const bool two = it.two;
+      const int tok_t = it.tok0 + (two ? t * tpt : 0);
+      const bool valid = rl < tpt * g && tok_t + rt < it.q_len;
+      const int n_other = t == 0 ? it.nt1 : it.nt0;
+      float w_own = 1.f, w_oth = 0.f;
+      if (!two) {
+        float (*ml)[2][128] = bars->ml[n_ml & 1];
+        ml[t][0][rl] = m_run;
+        ml[t][1][rl] = l_run;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->ml_full[t]);
+        if (!wait(&bars->ml_full[t ^ 1], n_ml++)) { ok = false; break; }
+        const float m2 = ml[t ^ 1][0][rl], l2 = ml[t ^ 1][1][rl];
+        const float m = fmaxf(m_run, m2);
+        if (m != -INFINITY) {
+          w_own = fast_exp2((m_run - m) * C::SCALE);
+          w_oth = fast_exp2((m2 - m) * C::SCALE);
+        }
+        l_run = l_run * w_own + l2 * w_oth;
+        m_run = m;
+      }
+      if (my > 0 && !wait(&bars->o_final[t], n_own)) { ok = false; break; }
+      if (!two && n_other > 0 && !wait(&bars->o_final[t ^ 1], n_oth)) { ok = false; break; }
+      n_own += my > 0;
+      n_oth += n_other > 0;
+      tc_fence_after();
+      const bool empty = l_run == 0.f;               // no visible key (a NaN sum is not zero)
+      const float inv = empty ? 0.f : 1.f / l_run;
+      const float lse = empty ? -INFINITY : ((m_run == -INFINITY ? 0.f : m_run * C::SCALE) + log2f(l_run)) * kLn2f;
+      w_own *= inv;
+      w_oth *= inv;
+      const bool odd = *reinterpret_cast<volatile int*>(&bars->odd[k & 1]) == k + 1;
+      const int64_t prow = (static_cast<int64_t>(it.part) * a.hkv + it.kvh) * a.tile_rows + (two ? t * tpt * g : 0) + rl;
+      const int rows = min(tpt, it.q_len - tok_t) * g;     // rows of this tile
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) +
+                           ((static_cast<int64_t>(it.row0) + tok_t) * a.hq + it.kvh * g) * D;
+      if (valid && (two || t == 0)) {
+        if (it.part >= 0) a.part_lse[prow] = lse;
+        else if (a.lse) a.lse[(static_cast<int64_t>(it.row0) + tok_t + rt) * a.hq + it.kvh * g + rh] = lse;
+      }
+      // 32 columns at a time; with one row tile each warpgroup writes half of them
+      const int c_lo = two ? 0 : t * (D / 2), c_hi = two ? D : c_lo + D / 2;
+#pragma unroll 1
+      for (int c = c_lo; c < c_hi; c += 32) {
+        uint32_t ov[32];
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        if (my > 0) {
+          tmem_ld_x32(o_tmem + c, ov);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(ov[e]) * w_own;
+        }
+        if (!two && n_other > 0) {
+          tmem_ld_x32(o_oth + c, ov);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] += __uint_as_float(ov[e]) * w_oth;
+        }
+        if (it.part >= 0) {
+          if (valid) {
+            float4* d4 = reinterpret_cast<float4*>(a.part_o + prow * D + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d4[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+        } else {
+          // through shared memory, so that a store writes 64-byte pieces of rows
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(pack2(v[8 * e], v[8 * e + 1]), pack2(v[8 * e + 2], v[8 * e + 3]),
+                           pack2(v[8 * e + 4], v[8 * e + 5]), pack2(v[8 * e + 6], v[8 * e + 7]));
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = 8 * x + (lane >> 2), ch = lane & 3, row = sub * 32 + r;
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+            const int tk = static_cast<int>((row * ginv) >> 16);
+            if (row < rows)
+              *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(tk) * a.hq + (row - tk * g)) * D + c + 8 * ch) = w;
+          }
+        }
+      }
+      if (odd) {
+        // columns with a non-finite value that this row sees: what the sum would be
+        __syncwarp();
+        const unsigned long long tag = static_cast<unsigned long long>(~static_cast<uint32_t>(k + 1)) << 32;
+        auto seen = [&](int kind, int col) {
+          const unsigned long long x = bars->first[k & 1][kind][col];
+          return (x & 0xffffffff00000000ull) == tag && static_cast<int>(x & 0xffffffffu) <= lim;
+        };
+        for (int c = c_lo; valid && c < c_hi; ++c) {
+          const bool pos = seen(0, c), neg = seen(1, c), nan = seen(2, c) || (pos && neg);
+          if (!pos && !neg && !nan) continue;
+          const float add = nan ? __int_as_float(0x7fc00000) : pos ? INFINITY : -INFINITY;
+          if (it.part >= 0) {
+            a.part_o[prow * D + c] += add;
+          } else {
+            __nv_bfloat16* x = out + (static_cast<int64_t>(rt) * a.hq + rh) * D + c;
+            *x = __float2bfloat16_rn(__bfloat162float(*x) + add);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_relaxed(&bars->done[k & 1]);   // O and the notes have been read
+    }
+    if (!ok) fail(9);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const int nbox = kKeyTile / p.box_rows;
@@ -488,221 +708,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       if (lane == 0) mbar_arrive(&bars->noted[k & 1]);
     }
     if (!ok && lane == 0) fail(11);
-  } else {
-    // -------------------------------------------------------------- softmax
-    const int t = warp >= 8 ? 1 : 0;
-    const int sub = warp & 3;
-    const int rl = sub * 32 + lane;
-    const uint32_t ginv = 65536u / g + 1;            // row / g for rows below 128, g <= 64: exact
-    const int rt = static_cast<int>((rl * ginv) >> 16), rh = rl - rt * g;   // token and head of this thread's row
-    const uint32_t s_tmem = tmem + (static_cast<uint32_t>(sub * 32) << 16) + t * 256;
-    const uint32_t o_tmem = s_tmem + 128;
-    const uint32_t o_oth = tmem + (static_cast<uint32_t>(sub * 32) << 16) + (t ^ 1) * 256 + 128;
-    const uint64_t sc2 = f2_pack(C::SCALE, C::SCALE);
-    uint8_t* stage = smem + C::OFF_OUT + (warp - 4) * 2048;
-    uint32_t n_s = 0, n_own = 0, n_oth = 0, n_ml = 0;   // phases: scores, both final O's, exchanged maxima
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      // (read again for the output, so that little of it is held in registers beside the scores)
-      int my, lim, lim_w, key_first, key_step;
-      {
-        if (!wait(&bars->work_full[k & 1], k >> 1)) { ok = false; break; }
-        Item it;
-        if (!get_item(bars, k, it)) break;
-        const int tok_t = it.tok0 + (it.two ? t * tpt : 0);   // first token of this warpgroup's rows
-        const bool valid = rl < tpt * g && tok_t + rt < it.q_len;
-        lim = valid ? it.ctx + tok_t + rt : it.kv_len - 1;                         // last visible key
-        lim_w = it.ctx + tok_t + static_cast<int>((sub * 32 * ginv) >> 16);           // the smallest of this warp's rows
-        my = t == 0 ? it.nt0 : it.nt1;
-        key_first = (it.kt0 + (it.two ? 0 : t)) * kKeyTile;
-        key_step = it.two ? kKeyTile : 2 * kKeyTile;
-      }
-      float m_run = -INFINITY, l_run = 0.f;
-      for (int i = 0; i < my; ++i) {
-        const int key0 = key_first + i * key_step;
-        if (!wait(&bars->s_full[t], n_s++)) { ok = false; break; }
-        tc_fence_after();
-        uint32_t sr[128];
-        tmem_ld_x128(s_tmem, sr);
-        if (key0 + kKeyTile - 1 > lim_w) {
-          const int rel = lim - key0;                      // columns <= rel are visible
-#pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (e > rel) sr[e] = __float_as_uint(-INFINITY);
-        }
-        float mx[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mx[e] = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 64; ++e)
-          mx[e & 7] = fmax3(mx[e & 7], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
-        const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
-        const float m_new = fmaxf(m_run, mt);
-        const bool need = (m_new - m_run) * C::SCALE > 8.f;   // lazy rescale: only when P could exceed 2^8
-        float alpha = 1.f;
-        if (need) {
-          alpha = fast_exp2((m_run - m_new) * C::SCALE);
-          m_run = m_new;
-        }
-        const float m_use = (m_run == -INFINITY) ? 0.f : m_run * C::SCALE;
-        const uint64_t nm2 = f2_pack(-m_use, -m_use);
-        uint64_t acc2[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc2[e] = 0ull;   // two 0.0f
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float x0, x1, p0, p1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])),
-                             sc2, nm2), x0, x1);
-            p0 = fast_exp2(x0);
-            p1 = fast_exp2(x1);
-            acc2[e & 3] = f2_add(acc2[e & 3], f2_pack(p0, p1));
-            pk[e] = pack2(p0, p1);
-          }
-          tmem_st_x16(s_tmem + 16 * c, pk);
-        }
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float a0, a1;
-          f2_unpack(acc2[e], a0, a1);
-          sum += a0 + a1;
-        }
-        l_run = l_run * alpha + sum;
-        if (i > 0 && __any_sync(0xffffffffu, need)) {
-          // O was last written by the previous PV, which completed before this
-          // S (the commit signalling S covers every earlier MMA).
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t ov[32];
-            tmem_ld_x32(o_tmem + 32 * c, ov);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-            tmem_st_x32(o_tmem + 32 * c, ov);
-          }
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[t]);
-      }
-      if (!ok) break;
-      // ---- the piece's output: its own O (two row tiles), or half of the
-      // columns of both O's joined (one)
-      if (!wait(&bars->noted[k & 1], k >> 1)) { ok = false; break; }
-      Item it;
-      get_item(bars, k, it);
-      const bool two = it.two;
-      const int tok_t = it.tok0 + (two ? t * tpt : 0);
-      const bool valid = rl < tpt * g && tok_t + rt < it.q_len;
-      const int n_other = t == 0 ? it.nt1 : it.nt0;
-      float w_own = 1.f, w_oth = 0.f;
-      if (!two) {
-        float (*ml)[2][128] = bars->ml[n_ml & 1];
-        ml[t][0][rl] = m_run;
-        ml[t][1][rl] = l_run;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->ml_full[t]);
-        if (!wait(&bars->ml_full[t ^ 1], n_ml++)) { ok = false; break; }
-        const float m2 = ml[t ^ 1][0][rl], l2 = ml[t ^ 1][1][rl];
-        const float m = fmaxf(m_run, m2);
-        if (m != -INFINITY) {
-          w_own = fast_exp2((m_run - m) * C::SCALE);
-          w_oth = fast_exp2((m2 - m) * C::SCALE);
-        }
-        l_run = l_run * w_own + l2 * w_oth;
-        m_run = m;
-      }
-      if (my > 0 && !wait(&bars->o_final[t], n_own)) { ok = false; break; }
-      if (!two && n_other > 0 && !wait(&bars->o_final[t ^ 1], n_oth)) { ok = false; break; }
-      n_own += my > 0;
-      n_oth += n_other > 0;
-      tc_fence_after();
-      const bool empty = l_run == 0.f;               // no visible key (a NaN sum is not zero)
-      const float inv = empty ? 0.f : 1.f / l_run;
-      const float lse = empty ? -INFINITY : ((m_run == -INFINITY ? 0.f : m_run * C::SCALE) + log2f(l_run)) * kLn2f;
-      w_own *= inv;
-      w_oth *= inv;
-      const bool odd = *reinterpret_cast<volatile int*>(&bars->odd[k & 1]) == k + 1;
-      const int64_t prow = (static_cast<int64_t>(it.part) * a.hkv + it.kvh) * a.tile_rows + (two ? t * tpt * g : 0) + rl;
-      const int rows = min(tpt, it.q_len - tok_t) * g;     // rows of this tile
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) +
-                           ((static_cast<int64_t>(it.row0) + tok_t) * a.hq + it.kvh * g) * D;
-      if (valid && (two || t == 0)) {
-        if (it.part >= 0) a.part_lse[prow] = lse;
-        else if (a.lse) a.lse[(static_cast<int64_t>(it.row0) + tok_t + rt) * a.hq + it.kvh * g + rh] = lse;
-      }
-      // 32 columns at a time; with one row tile each warpgroup writes half of them
-      const int c_lo = two ? 0 : t * (D / 2), c_hi = two ? D : c_lo + D / 2;
-#pragma unroll 1
-      for (int c = c_lo; c < c_hi; c += 32) {
-        uint32_t ov[32];
-        float v[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = 0.f;
-        if (my > 0) {
-          tmem_ld_x32(o_tmem + c, ov);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(ov[e]) * w_own;
-        }
-        if (!two && n_other > 0) {
-          tmem_ld_x32(o_oth + c, ov);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] += __uint_as_float(ov[e]) * w_oth;
-        }
-        if (it.part >= 0) {
-          if (valid) {
-            float4* d4 = reinterpret_cast<float4*>(a.part_o + prow * D + c);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d4[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-          }
-        } else {
-          // through shared memory, so that a store writes 64-byte pieces of rows
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(pack2(v[8 * e], v[8 * e + 1]), pack2(v[8 * e + 2], v[8 * e + 3]),
-                           pack2(v[8 * e + 4], v[8 * e + 5]), pack2(v[8 * e + 6], v[8 * e + 7]));
-          __syncwarp();
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int r = 8 * x + (lane >> 2), ch = lane & 3, row = sub * 32 + r;
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
-            const int tk = static_cast<int>((row * ginv) >> 16);
-            if (row < rows)
-              *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(tk) * a.hq + (row - tk * g)) * D + c + 8 * ch) = w;
-          }
-        }
-      }
-      if (odd) {
-        // columns with a non-finite value that this row sees: what the sum would be
-        __syncwarp();
-        const unsigned long long tag = static_cast<unsigned long long>(~static_cast<uint32_t>(k + 1)) << 32;
-        auto seen = [&](int kind, int col) {
-          const unsigned long long x = bars->first[k & 1][kind][col];
-          return (x & 0xffffffff00000000ull) == tag && static_cast<int>(x & 0xffffffffu) <= lim;
-        };
-        for (int c = c_lo; valid && c < c_hi; ++c) {
-          const bool pos = seen(0, c), neg = seen(1, c), nan = seen(2, c) || (pos && neg);
-          if (!pos && !neg && !nan) continue;
-          const float add = nan ? __int_as_float(0x7fc00000) : pos ? INFINITY : -INFINITY;
-          if (it.part >= 0) {
-            a.part_o[prow * D + c] += add;
-          } else {
-            __nv_bfloat16* x = out + (static_cast<int64_t>(rt) * a.hq + rh) * D + c;
-            *x = __float2bfloat16_rn(__bfloat162float(*x) + add);
-          }
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_relaxed(&bars->done[k & 1]);   // O and the notes have been read
-    }
-    if (!ok) fail(9);
+  }
   }
   tc_fence_before();
   __syncthreads();
