@@ -102,6 +102,7 @@ struct AttendArgs {
   int32_t small_rows;             // requests of at most so many rows go to the decode kernel
   int32_t tiles;                  // whether a tile kernel runs
   int32_t slots;                  // blocks of it that run at once
+  float piece_cost, merge_cost;   // fixed costs of a piece and of cutting, in key tiles
   int32_t piece_cap;              // pieces the workspace has room for
   int32_t part_cap;               // partial results it has room for, per kv head; 0: never cut
   int32_t item_cap;

@@ -17,10 +17,8 @@ namespace pa {
 namespace {
 
 constexpr int kBuckets = 256;
-// A piece's fixed cost (prologue, first copies in flight, epilogue) in key
-// tiles.  Cutting keys is looked at while the rows give less than three waves
-// of blocks: from there on there is nothing to gain.
-constexpr int kPieceCost = 5;
+// Cutting keys is looked at while the rows give less than three waves of
+// blocks: from there on there is nothing to gain.
 constexpr int kCuts = 32;
 constexpr int kMaxCut = 64;
 constexpr int kMaxCutItems = 1024;
@@ -181,17 +179,18 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
         p = max(p, 1);
         np += p;
         nc += p > 1 ? p : 0;
-        load += d + kPieceCost * p;
+        load += d;
       }
       atomicAdd(&cost_pieces[lane], np);
       atomicAdd(&cost_cuts[lane], nc);
       atomicAdd(&cost_load[lane], load);
       __syncthreads();
       if (warp == 0) {
-        float cost = static_cast<float>(kPieceCost + c);
+        const float piece = a.piece_cost + c;   // the longest piece
+        float cost = piece;
         if (static_cast<int64_t>(cost_pieces[lane]) * a.hkv > a.slots)
-          cost = fmaxf(cost, static_cast<float>(cost_load[lane]) * a.hkv / a.slots + 0.5f * (kPieceCost + c));
-        if (cuts > 1) cost += 3.f + cuts / 8.f;
+          cost = fmaxf(cost, (cost_load[lane] + a.piece_cost * cost_pieces[lane]) * a.hkv / a.slots + 0.5f * piece);
+        if (cuts > 1) cost += a.merge_cost * (1.f + cuts / 24.f);
         if (cost_cuts[lane] > a.part_cap || cuts > deepest) cost = INFINITY;
         const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));
         const unsigned who = __ballot_sync(0xffffffffu, __float_as_uint(cost) == least);
@@ -397,11 +396,17 @@ size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws) {
     a.tile_rows = 256;                // two tiles of 128 rows
     a.tile_tokens = 2 * (128 / g);
     a.slots = kSms;
+    // in key tiles of 2.1 us: a piece's set-up and output, the merge's launch
+    a.piece_cost = 5.f;
+    a.merge_cost = 3.f;
   } else {
     // fp32 rows per block: 16 when no request has more, 64 otherwise
     a.tile_rows = a.max_q > 0 && static_cast<int64_t>(a.max_q) * g <= 16 ? 16 : 64;
     a.tile_tokens = a.tile_rows / g;
     a.slots = simt_blocks_per_sm(a) * kSms;
+    // in key tiles of about 10 us with 64 rows, 3 us with 16
+    a.piece_cost = a.tile_rows == 16 ? 1.f : 0.3f;
+    a.merge_cost = a.tile_rows == 16 ? 2.f : 0.6f;
   }
   // Rows per kv head up to which a request is the decode kernel's.  A call
   // whose requests are long on average leaves them all to the tile kernel:

@@ -30,6 +30,16 @@ struct SimtCfg {
   static constexpr int SMEM = FLOATS * 4 + 2 * kKeys * 8;
 };
 
+// two fp32 FMAs in one instruction (half the issue slots)
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+        "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
 __device__ __forceinline__ void copy16(float* dst, const float* src, bool valid) {
   const int n = valid ? 16 : 0;   // 0: fill the 16 bytes with zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
@@ -39,7 +49,7 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool valid)
 }
 
 template <int D, int ROWS>
-__global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(256, 2) attend_simt_kernel(AttendArgs a) {
   using C = SimtCfg<D, ROWS>;
   constexpr int R = ROWS / 16, CV = D / 64;      // rows, float4 columns of a thread
   extern __shared__ __align__(16) float sm[];
@@ -96,7 +106,8 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
   __syncthreads();
   fetch(0);
   int64_t lim[R];                                // last visible key of each row
-  float m_run[R], l_run[R], acc[R][4 * CV];
+  float m_run[R], l_run[R];
+  float2 acc[R][2 * CV];                         // columns 64 j + 4 tx .. + 3 of each row
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int r = ty * R + i;
@@ -104,7 +115,7 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
     m_run[i] = -INFINITY;
     l_run[i] = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4 * CV; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < 2 * CV; ++j) acc[i][j] = make_float2(0.f, 0.f);
   }
   const int64_t lim_first = static_cast<int64_t>(pc.kv_len) - pc.q_len + pc.tok0;
   int st = 0;
@@ -118,9 +129,12 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
     const float* sk = sm + C::OFF_KV + st * C::STAGE;
     const float* sv = sk + kKeys * C::LDK;
     // scores of rows ty * R + i and keys tx + 16 * j
-    float s[R][4];
+    // (even and odd columns summed apart, two FMAs to an instruction)
+    float2 s2[R][4];
 #pragma unroll
-    for (int i = 0; i < R; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int m = 0; m < D; m += 4) {
       float4 q4[R], k4[4];
@@ -132,12 +146,15 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
       for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[i][j] = fmaf(q4[i].x, k4[j].x, s[i][j]);
-          s[i][j] = fmaf(q4[i].y, k4[j].y, s[i][j]);
-          s[i][j] = fmaf(q4[i].z, k4[j].z, s[i][j]);
-          s[i][j] = fmaf(q4[i].w, k4[j].w, s[i][j]);
+          s2[i][j] = fma2(make_float2(q4[i].x, q4[i].y), make_float2(k4[j].x, k4[j].y), s2[i][j]);
+          s2[i][j] = fma2(make_float2(q4[i].z, q4[i].w), make_float2(k4[j].z, k4[j].w), s2[i][j]);
         }
     }
+    float s[R][4];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
     // (before the stores below: a tile that every row sees in full needs no mask)
     const bool whole = c0 + kKeys - 1 <= lim_first;
 #pragma unroll
@@ -164,7 +181,10 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
       for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       l_run[i] = l_run[i] * alpha + sum;
 #pragma unroll
-      for (int j = 0; j < 4 * CV; ++j) acc[i][j] *= alpha;
+      for (int j = 0; j < 2 * CV; ++j) {
+        acc[i][j].x *= alpha;
+        acc[i][j].y *= alpha;
+      }
     }
     __syncwarp();   // a row's 16 threads are in one warp
     if (whole) {
@@ -181,10 +201,9 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
             const float4 v4 = *reinterpret_cast<const float4*>(sv + (key + k) * D + 64 * j + 4 * tx);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-              acc[i][4 * j] = fmaf(p[i][k], v4.x, acc[i][4 * j]);
-              acc[i][4 * j + 1] = fmaf(p[i][k], v4.y, acc[i][4 * j + 1]);
-              acc[i][4 * j + 2] = fmaf(p[i][k], v4.z, acc[i][4 * j + 2]);
-              acc[i][4 * j + 3] = fmaf(p[i][k], v4.w, acc[i][4 * j + 3]);
+              const float2 pp = make_float2(p[i][k], p[i][k]);
+              acc[i][2 * j] = fma2(pp, make_float2(v4.x, v4.y), acc[i][2 * j]);
+              acc[i][2 * j + 1] = fma2(pp, make_float2(v4.z, v4.w), acc[i][2 * j + 1]);
             }
           }
       }
@@ -200,10 +219,9 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
           for (int i = 0; i < R; ++i)
             if (c0 + key <= lim[i]) {
               const float p = sp[(ty * R + i) * C::LDP + key];
-              acc[i][4 * j] = fmaf(p, v4.x, acc[i][4 * j]);
-              acc[i][4 * j + 1] = fmaf(p, v4.y, acc[i][4 * j + 1]);
-              acc[i][4 * j + 2] = fmaf(p, v4.z, acc[i][4 * j + 2]);
-              acc[i][4 * j + 3] = fmaf(p, v4.w, acc[i][4 * j + 3]);
+              const float2 pp = make_float2(p, p);
+              acc[i][2 * j] = fma2(pp, make_float2(v4.x, v4.y), acc[i][2 * j]);
+              acc[i][2 * j + 1] = fma2(pp, make_float2(v4.z, v4.w), acc[i][2 * j + 1]);
             }
         }
       }
@@ -224,7 +242,7 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttendArgs a) {
 #pragma unroll
     for (int j = 0; j < CV; ++j)
       *reinterpret_cast<float4*>(dst + 64 * j + 4 * tx) =
-          make_float4(acc[i][4 * j] * inv, acc[i][4 * j + 1] * inv, acc[i][4 * j + 2] * inv, acc[i][4 * j + 3] * inv);
+          make_float4(acc[i][2 * j].x * inv, acc[i][2 * j].y * inv, acc[i][2 * j + 1].x * inv, acc[i][2 * j + 1].y * inv);
     if (tx == 0) {
       if (pc.part >= 0) a.part_lse[part] = lse;
       else if (a.lse) a.lse[row] = lse;
