@@ -144,7 +144,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
   const int64_t u_lo = ds.first;
   auto block_of = [&](int64_t u) {   // the block whose range holds group u
     const int64_t cut = ds.more * (ds.each + 1);
-    return u < cut ? u / (ds.each + 1) : ds.more + (u - cut) / ds.each;
+    if ((u >> 31) == 0) {            // (32-bit divisions, unless there are that many groups)
+      const uint32_t v = static_cast<uint32_t>(u), e = static_cast<uint32_t>(ds.each);
+      return u < cut ? static_cast<int>(v / (e + 1)) : ds.more + static_cast<int>((v - static_cast<uint32_t>(cut)) / e);
+    }
+    return static_cast<int>(u < cut ? u / (ds.each + 1) : ds.more + (u - cut) / ds.each);
   };
   const int64_t max_kv = static_cast<int64_t>(a.max_pages) * a.page_size;
   const int g = a.hq / a.hkv;
@@ -358,9 +362,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
     __syncthreads();
     // the range of blocks that share this pair's keys
     const int64_t item_lo = u_lo + it - cur.unit;
-    const int c_lo = static_cast<int>(block_of(item_lo));
-    const int c_hi = static_cast<int>(block_of(item_lo + cur.n_units - 1));
-    const bool whole = c_lo == c_hi;
+    const bool whole = item_lo >= u_lo && item_lo + cur.n_units <= u_lo + steps;
+    const int c_lo = whole || item_lo >= u_lo ? static_cast<int>(blockIdx.x) : block_of(item_lo);
+    const int c_hi = whole || item_end ? static_cast<int>(blockIdx.x) : block_of(item_lo + cur.n_units - 1);
     // a block's partial slots: 0 for a pair that begins before its range, 1 for one that begins in it
     auto slot_of = [&](int c) { return 2 * c + (c == c_lo ? 1 : 0); };
     const int64_t out0 = static_cast<int64_t>(slot_of(blockIdx.x)) * 16;
@@ -411,29 +415,50 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
       }
     }
     if (!whole) {
-      __threadfence();
       __syncthreads();
-      if (threadIdx.x == 0) flag[1] = atomicAdd(&a.done[c_lo], 1) == c_hi - c_lo;
+      if (threadIdx.x == 0) {
+        __threadfence();   // the whole block's part, behind the barrier
+        const bool last = atomicAdd(&a.done[c_lo], 1) == c_hi - c_lo;
+        if (last) __threadfence();   // the other blocks' parts
+        flag[1] = last;
+      }
       __syncthreads();
       if (flag[1]) {
-        __threadfence();
+        // the last to arrive: all parts, in order, four at a time (their
+        // loads go out together; an online softmax over the groups of four)
         const int parts = c_hi - c_lo + 1;
         for (int i = threadIdx.x; i < rows * C::CH; i += kWarps * 32) {
           const int r = i / C::CH, c = i % C::CH;
-          float M = -INFINITY;
-          for (int p = 0; p < parts; ++p) M = fmaxf(M, __ldcg(a.dec_lse + slot_of(c_lo + p) * 16 + r));
-          const float sub = M == -INFINITY ? 0.f : M;
-          float L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-          for (int p = 0; p < parts; ++p) {
-            const int64_t at = static_cast<int64_t>(slot_of(c_lo + p)) * 16 + r;
-            const float f = expf(__ldcg(a.dec_lse + at) - sub);
-            L += f;
-            const float4* src = reinterpret_cast<const float4*>(a.dec_o + at * D + 8 * c);
-            const float4 x = __ldcg(src), y = __ldcg(src + 1);
-            if (f != 0.f) {   // (a part without a visible key)
-              acc[0] += f * x.x; acc[1] += f * x.y; acc[2] += f * x.z; acc[3] += f * x.w;
-              acc[4] += f * y.x; acc[5] += f * y.y; acc[6] += f * y.z; acc[7] += f * y.w;
+          float M = -INFINITY, L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          for (int p0 = 0; p0 < parts; p0 += 4) {
+            float ls[4];
+            float4 x[4], y[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              ls[p] = -INFINITY;
+              if (p0 + p < parts) {
+                const int64_t at = static_cast<int64_t>(slot_of(c_lo + p0 + p)) * 16 + r;
+                const float4* src = reinterpret_cast<const float4*>(a.dec_o + at * D + 8 * c);
+                ls[p] = __ldcg(a.dec_lse + at);
+                x[p] = __ldcg(src);
+                y[p] = __ldcg(src + 1);
+              }
+            }
+            const float m = fmaxf(fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3])), M);
+            const float sub = m == -INFINITY ? 0.f : m;
+            const float old = expf(M - sub);
+            M = m;
+            L *= old;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] *= old;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              const float f = expf(ls[p] - sub);
+              L += f;
+              if (p0 + p < parts && f != 0.f) {   // (zero: a part without a visible key)
+                acc[0] += f * x[p].x; acc[1] += f * x[p].y; acc[2] += f * x[p].z; acc[3] += f * x[p].w;
+                acc[4] += f * y[p].x; acc[5] += f * y[p].y; acc[6] += f * y[p].z; acc[7] += f * y[p].w;
+              }
             }
           }
           const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -441,7 +466,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
           *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + row * D + 8 * c) =
               make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
                          pack_bf16(acc[4] * inv, acc[5] * inv), pack_bf16(acc[6] * inv, acc[7] * inv));
-          if (c == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : sub + logf(L);
+          if (c == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) + logf(L);
         }
       }
     }

@@ -74,7 +74,7 @@ struct SvBars {
   uint64_t s_full[2], p_full[2], o_final[2];
   uint64_t noted[2];      // the guard is through with a piece's tiles; pieces in turn
   uint64_t done[2];       // the softmax warps have read a piece's O and notes; pieces in turn
-  uint64_t ml_full[2];    // a warpgroup's maxima and sums are written (one row tile)
+  uint64_t ml_full[2][2]; // a warpgroup's maxima and sums are written (one row tile); pieces in turn
   uint64_t work_full[2];  // `work` holds a piece; pieces in turn
   uint64_t drain;
   uint32_t tmem_base;
@@ -83,7 +83,7 @@ struct SvBars {
   // per column: first key with +inf, -inf, NaN, below the complement of 1 + the
   // piece's number, so that a later piece's entry is always the smaller
   unsigned long long first[2][3][128];
-  float ml[2][2][2][128]; // [in turn][warpgroup][maximum, sum][row]
+  float ml[2][2][2][128]; // [pieces in turn][warpgroup][maximum, sum][row]
   struct {
     int4 rows;            // row0, tok0, q_len, kv_len
     int4 keys;            // kt0, n, part, kvh (-1: no more)
@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       mbar_init(&bars->o_final[s], 1);
       mbar_init(&bars->noted[s], 2);
       mbar_init(&bars->done[s], 8);
-      mbar_init(&bars->ml_full[s], 4);
+      mbar_init(&bars->ml_full[s][0], 4);
+      mbar_init(&bars->ml_full[s][1], 4);
       mbar_init(&bars->work_full[s], 1);
       bars->odd[s] = 0;
     }
@@ -265,7 +266,8 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
     const uint32_t o_oth = tmem + (static_cast<uint32_t>(sub * 32) << 16) + (t ^ 1) * 256 + 128;
     const uint64_t sc2 = f2_pack(C::SCALE, C::SCALE);
     uint8_t* stage = smem + C::OFF_OUT + (warp - 4) * 2048;
-    uint32_t n_s = 0, n_own = 0, n_oth = 0, n_ml = 0;   // phases: scores, both final O's, exchanged maxima
+    uint32_t n_s = 0, n_own = 0, n_oth = 0;   // phases: scores, both final O's
+    uint32_t ph_ml = 0;                       // and of both pairs of exchanged maxima, one bit each
     bool ok = true;
     for (int k = 0; ok; ++k) {
       // (read again for the output, so that little of it is held in registers beside the scores)
@@ -366,12 +368,13 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       const int n_other = t == 0 ? it.nt1 : it.nt0;
       float w_own = 1.f, w_oth = 0.f;
       if (!two) {
-        float (*ml)[2][128] = bars->ml[n_ml & 1];
+        float (*ml)[2][128] = bars->ml[k & 1];
         ml[t][0][rl] = m_run;
         ml[t][1][rl] = l_run;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->ml_full[t]);
-        if (!wait(&bars->ml_full[t ^ 1], n_ml++)) { ok = false; break; }
+        if (lane == 0) mbar_arrive(&bars->ml_full[k & 1][t]);
+        if (!wait(&bars->ml_full[k & 1][t ^ 1], ph_ml >> (k & 1))) { ok = false; break; }
+        ph_ml ^= 1u << (k & 1);
         const float m2 = ml[t ^ 1][0][rl], l2 = ml[t ^ 1][1][rl];
         const float m = fmaxf(m_run, m2);
         if (m != -INFINITY) {
