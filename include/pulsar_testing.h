@@ -43,6 +43,21 @@ int pa_testing_phase2_stall(const void* q, const void* k_ret, const void* v_ret,
                             int64_t T, int32_t n_shards, int32_t hq, int32_t hkv, int32_t d, void* o,
                             float* lse, void* ws, size_t ws_bytes, int32_t wait_limit_us, void* stream);
 
+/*
+ * Runs pa_paged_attend (pulsar_serving.h) on bf16 inputs with every bounded
+ * device wait limited to wait_limit_us microseconds (1 .. 10^7) and one barrier
+ * per block made unsatisfiable in the same way: the Q barrier of the tile
+ * kernel (max_q * hq / hkv > 16), each warp's first key copy in the decode
+ * kernel.  Every block records PA_ERR_TIMEOUT, drains its copies and MMAs and
+ * returns; the context stays usable.  Arguments as pa_paged_attend (lse not
+ * written); the outputs are unspecified.
+ */
+int pa_testing_paged_stall(const void* q, int64_t N, const int32_t* cu_q, const int32_t* kv_len, int32_t B,
+                           int32_t max_q, const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                           const void* k_pages, const void* v_pages, int32_t n_pages, int32_t hq,
+                           int32_t hkv, int32_t d, void* o, void* ws, size_t ws_bytes,
+                           int32_t wait_limit_us, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

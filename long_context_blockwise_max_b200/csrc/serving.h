@@ -118,6 +118,7 @@ struct AttendArgs {
   float* dec_o;                   // [2 * decode_ctas][16][d]
   float* dec_lse;                 // [2 * decode_ctas][16]
   uint64_t wait_limit_ns = 1000000000ull;
+  int stall = 0;                  // test only: one barrier per block expects 16 bytes more than are copied
 };
 // Fills the plan's sizes and returns the workspace bytes; with `ws` set,
 // carves it.  `max_kv` is the longest cache a request may have.

@@ -4,10 +4,13 @@
 #include <cmath>
 
 #include "serving.h"
+#include "../../include/pulsar_testing.h"
 
 using namespace pa;
 
 namespace {
+
+constexpr uint64_t kWaitLimitNs = 1000000000ull;   // of every bounded device wait
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -62,8 +65,48 @@ AttendArgs attend_args(int dtype, int64_t N, int32_t B, int32_t max_q, int32_t m
   a.max_pages = max_pages; a.page_size = page_size;
   a.page_shift = log2_of(page_size);
   a.hq = hq; a.hkv = hkv; a.d = d;
-  a.wait_limit_ns = 1000000000ull;
+  a.wait_limit_ns = kWaitLimitNs;
   return a;
+}
+
+int paged_attend(const void* q, int dtype, int64_t N, int64_t ldq, const int32_t* cu_q, const int32_t* kv_len,
+                    int32_t B, int32_t max_q, const int32_t* block_table, int64_t table_stride,
+                    int32_t max_pages, int32_t page_size, const void* k_pages, const void* v_pages,
+                    int32_t n_pages, int32_t hq, int32_t hkv, int32_t d, void* o, float* lse_opt, void* ws,
+                    size_t ws_bytes, void* stream, uint64_t wait_limit_ns, int stall) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int rc = check_heads(hq, hkv, d, dtype);
+  if (!rc) rc = check_batch(B, N);
+  if (!rc) rc = check_pages(max_pages, page_size);
+  if (rc) return rc;
+  if (max_q < 1 || n_pages < 0 || !cu_q || (B > 1 && table_stride < max_pages)) return PA_ERR_INVALID;
+  if (static_cast<int64_t>(n_pages) * page_size > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (B > 0 && N > 0) {
+    if (!q || !o || !kv_len || !block_table) return PA_ERR_INVALID;
+    if (n_pages > 0 && (!k_pages || !v_pages)) return PA_ERR_INVALID;
+    rc = check_ld(ldq, hq, d, dtype);
+    if (rc) return rc;
+  }
+  const void* ptrs[] = {q, k_pages, v_pages, o};
+  for (const void* p : ptrs)
+    if (p && !aligned(p, 16)) return PA_ERR_UNSUPPORTED;
+  const int64_t max_kv = static_cast<int64_t>(max_pages) * page_size;
+  AttendArgs a = attend_args(dtype, N, B, max_q, max_pages, page_size, hq, hkv, d);
+  rc = check_ws(ws, ws_bytes, plan_attend(a, max_kv, nullptr));
+  if (rc) return rc;
+  plan_attend(a, max_kv, ws);
+  if (static_cast<int64_t>(a.piece_cap) * hkv > INT32_MAX) return PA_ERR_UNSUPPORTED;   // blocks of one launch
+  if (B == 0 || N == 0) return clear_status(ws, s);
+  a.q = q; a.k = k_pages; a.v = v_pages;
+  a.ldq = ldq;
+  a.ldk = a.ldv = static_cast<int64_t>(hkv) * d;
+  a.n_slots = static_cast<int64_t>(n_pages) * page_size;
+  a.cu_q = cu_q; a.kv_len = kv_len;
+  a.block_table = block_table; a.table_stride = table_stride;
+  a.o = o; a.lse = lse_opt;
+  a.wait_limit_ns = wait_limit_ns;
+  a.stall = stall;
+  return launch_attend(a, s);
 }
 
 }  // namespace
@@ -112,8 +155,10 @@ int pa_paged_append(const void* q, const void* k, const void* v, int dtype, int6
   if (!std::isfinite(rope_theta) || rope_theta < 0) return PA_ERR_INVALID;
   if (n_slots < 0 || n_slots > INT32_MAX) return PA_ERR_INVALID;
   const bool pages = slots != nullptr;
-  if (pages != (k_pages != nullptr) || pages != (v_pages != nullptr)) return PA_ERR_INVALID;
   if (N > 0) {
+    // (an empty cache may have no address)
+    if (pages ? n_slots > 0 && (!k_pages || !v_pages) : k_pages != nullptr || v_pages != nullptr)
+      return PA_ERR_INVALID;
     if (!k || (pages && !v) || (rope_theta > 0 && !positions)) return PA_ERR_INVALID;
     if ((q == nullptr) != (q_out == nullptr)) return PA_ERR_INVALID;
     if (q) rc = check_ld(ldq, hq, d, dtype);
@@ -190,37 +235,18 @@ int pa_paged_attend(const void* q, int dtype, int64_t N, int64_t ldq, const int3
                     int32_t max_pages, int32_t page_size, const void* k_pages, const void* v_pages,
                     int32_t n_pages, int32_t hq, int32_t hkv, int32_t d, void* o, float* lse_opt, void* ws,
                     size_t ws_bytes, void* stream) {
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int rc = check_heads(hq, hkv, d, dtype);
-  if (!rc) rc = check_batch(B, N);
-  if (!rc) rc = check_pages(max_pages, page_size);
-  if (rc) return rc;
-  if (max_q < 1 || n_pages < 0 || !cu_q || (B > 1 && table_stride < max_pages)) return PA_ERR_INVALID;
-  if (static_cast<int64_t>(n_pages) * page_size > INT32_MAX) return PA_ERR_UNSUPPORTED;
-  if (B > 0 && N > 0) {
-    if (!q || !o || !kv_len || !block_table) return PA_ERR_INVALID;
-    if (n_pages > 0 && (!k_pages || !v_pages)) return PA_ERR_INVALID;
-    rc = check_ld(ldq, hq, d, dtype);
-    if (rc) return rc;
-  }
-  const void* ptrs[] = {q, k_pages, v_pages, o};
-  for (const void* p : ptrs)
-    if (p && !aligned(p, 16)) return PA_ERR_UNSUPPORTED;
-  const int64_t max_kv = static_cast<int64_t>(max_pages) * page_size;
-  AttendArgs a = attend_args(dtype, N, B, max_q, max_pages, page_size, hq, hkv, d);
-  rc = check_ws(ws, ws_bytes, plan_attend(a, max_kv, nullptr));
-  if (rc) return rc;
-  plan_attend(a, max_kv, ws);
-  if (static_cast<int64_t>(a.piece_cap) * hkv > INT32_MAX) return PA_ERR_UNSUPPORTED;   // blocks of one launch
-  if (B == 0 || N == 0) return clear_status(ws, s);
-  a.q = q; a.k = k_pages; a.v = v_pages;
-  a.ldq = ldq;
-  a.ldk = a.ldv = static_cast<int64_t>(hkv) * d;
-  a.n_slots = static_cast<int64_t>(n_pages) * page_size;
-  a.cu_q = cu_q; a.kv_len = kv_len;
-  a.block_table = block_table; a.table_stride = table_stride;
-  a.o = o; a.lse = lse_opt;
-  return launch_attend(a, s);
+  return paged_attend(q, dtype, N, ldq, cu_q, kv_len, B, max_q, block_table, table_stride, max_pages, page_size,
+                      k_pages, v_pages, n_pages, hq, hkv, d, o, lse_opt, ws, ws_bytes, stream, kWaitLimitNs, 0);
+}
+
+int pa_testing_paged_stall(const void* q, int64_t N, const int32_t* cu_q, const int32_t* kv_len, int32_t B,
+                           int32_t max_q, const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                           const void* k_pages, const void* v_pages, int32_t n_pages, int32_t hq, int32_t hkv,
+                           int32_t d, void* o, void* ws, size_t ws_bytes, int32_t wait_limit_us, void* stream) {
+  if (wait_limit_us <= 0 || wait_limit_us > 10000000) return PA_ERR_INVALID;
+  return paged_attend(q, PA_BF16, N, static_cast<int64_t>(hq) * d, cu_q, kv_len, B, max_q, block_table, max_pages,
+                      max_pages, page_size, k_pages, v_pages, n_pages, hq, hkv, d, o, nullptr, ws, ws_bytes, stream,
+                      static_cast<uint64_t>(wait_limit_us) * 1000ull, 1);
 }
 
 }  // extern "C"

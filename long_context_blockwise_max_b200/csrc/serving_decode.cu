@@ -165,11 +165,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
   int row = look_up();
   int issued = 0;
   auto issue = [&](int it) {
-    if (it >= steps || flag[2]) return;
+    if (it >= steps || __any_sync(0xffffffffu, flag[2])) return;   // (one answer for the warp)
     ++issued;
     uint8_t* dst = ring + (it % kStages) * C::STAGE;
     uint64_t* bar = &full[it % kStages];
-    if (lane == 0) mbar_arrive_expect_tx(bar, C::STAGE);
+    if (lane == 0) mbar_arrive_expect_tx(bar, C::STAGE + (a.stall && it == 0 ? 16 : 0));
     __syncwarp();
     if (lane < nbox)
 #pragma unroll

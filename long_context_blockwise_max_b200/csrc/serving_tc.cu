@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       if (k > 0 && !wait(&bars->q_empty, k - 1)) { ok = false; break; }
       if (lane == 0) {
         const int qt = it.two ? 2 : 1;
-        mbar_arrive_expect_tx(&bars->q_full, qt * q_bytes);
+        mbar_arrive_expect_tx(&bars->q_full, qt * q_bytes + (a.stall ? 16 : 0));
         for (int t = 0; t < qt; ++t)
           for (int kb = 0; kb < C::NKB; ++kb)
             tma_load_3d(sQ + t * C::TILE_BYTES + kb * C::KB_BYTES, &tmQ, &bars->q_full, kb * 64, it.kvh * g,

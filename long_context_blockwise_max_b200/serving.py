@@ -54,6 +54,9 @@ def _declare():
         "pa_paged_attend": (INT, [P, INT, I64, I64, P, P, I32, I32, P, I64, I32, I32, P, P, I32, I32, I32, I32, P, P,
                                   P, SZ, P]),
     }
+    # test hook (include/pulsar_testing.h)
+    sig["pa_testing_paged_stall"] = (INT, [P, I64, P, P, I32, I32, P, I32, I32, P, P, I32, I32, I32, I32, P, P, SZ, I32,
+                                           P])
     for name, (res, args) in sig.items():
         fn = getattr(_lib, name)
         fn.restype, fn.argtypes = res, args
@@ -252,6 +255,8 @@ def pa_paged_append(q, k_new, v_new, positions, slots, k_pages, v_pages, rope_th
 
 def _attend_outputs(q, o, lse, want_lse):
     N, hq, d = q.shape
+    if o is not None and N > 0 and o.data_ptr() == q.data_ptr():
+        raise ValueError("o: must not be q")
     _need(o, "o", q.dtype, N * hq * d)
     _need(lse, "lse", torch.float32, N * hq)
     _dense(("o", o), ("lse", lse))
@@ -331,3 +336,20 @@ def pa_paged_attend(q, cu_q, kv_len, block_table, k_pages, v_pages, max_q: int, 
     _call(_lib.pa_paged_attend, q, ws, _p(q), dt, N, ldq, _p(cu_q), _p(kv_len), B, int(max_q), _p(block_table), stride,
           block_table.shape[1], page_size, _p(k_pages), _p(v_pages), n_pages, hq, hkv, d, _p(o), _p(lse))
     return o, lse, ws
+
+
+def pa_testing_paged_stall(q, cu_q, kv_len, block_table, k_pages, v_pages, max_q: int, wait_limit_us: int):
+    """Test hook: ``pa_paged_attend`` (bf16, dense tensors) with one
+    unsatisfiable barrier per block and waits limited to ``wait_limit_us``; the
+    workspace status then reads PA_ERR_TIMEOUT.  Returns the workspace."""
+    _on(q, cu_q, kv_len, block_table, k_pages, v_pages)
+    N, hq, d = q.shape
+    n_pages, page_size, hkv, _ = k_pages.shape
+    B, width = _batch(cu_q), block_table.shape[1]
+    o = torch.empty_like(q)
+    ws = _ws(pa_paged_attend_workspace_size(B, N, int(max_q), width, page_size, hq, hkv, d, pulsar.PA_BF16), q, None)
+    rc = _lib.pa_testing_paged_stall(_p(q), N, _p(cu_q), _p(kv_len), B, int(max_q), _p(block_table), width, page_size,
+                                     _p(k_pages), _p(v_pages), n_pages, hq, hkv, d, _p(o), _p(ws), ws.numel(),
+                                     int(wait_limit_us), torch.cuda.current_stream(q.device).cuda_stream)
+    _check(rc, "pa_testing_paged_stall")
+    return ws

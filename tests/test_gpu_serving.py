@@ -374,6 +374,77 @@ def test_paged_strided_rows_and_table(S):
     assert ok(S, ws) == 0 and torch.equal(o, o0) and torch.equal(lse, lse0)
 
 
+@pytest.mark.parametrize("page", [256, 1024, 32768])
+def test_paged_large_pages(S, page):
+    for case in (([1, 1, 2], [700, 1, 300]), ([90, 1], [700, 300])):
+        c = paged_batch(*case, 8, 2, 64, page, torch.bfloat16, seed=page)
+        o, lse, ws = S.pa_paged_attend(c["q"], c["cu_q"], c["kv_len"], c["table"], c["k_pages"], c["v_pages"], c["max_q"])
+        assert ok(S, ws) == 0
+        check_paged(c, o, lse, f"page {page}")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_paged_the_most_requests(S, dtype):
+    rng = np.random.default_rng(2)
+    kv = rng.integers(0, 40, 8192)
+    q = np.where(rng.random(8192) < 0.9, 1, 0)
+    c = paged_batch(q.tolist(), kv.tolist(), 4, 2, 64, 16, DTYPES[dtype], seed=2)
+    o, lse, ws = S.pa_paged_attend(c["q"], c["cu_q"], c["kv_len"], c["table"], c["k_pages"], c["v_pages"], 1)
+    assert ok(S, ws) == 0
+    check_paged(c, o, lse, "8192 requests")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [300, 200]), ([4], [300]), ([70], [400]), ([200], [200])])
+def test_a_bad_query_row_touches_no_other(S, dtype, bad, q_lens, kv_lens):
+    c = paged_batch(q_lens, kv_lens, 8, 2, 64, 16, DTYPES[dtype], seed=21)
+    args = (c["cu_q"], c["kv_len"], c["table"], c["k_pages"], c["v_pages"], c["max_q"])
+    o0, lse0, _ = S.pa_paged_attend(c["q"], *args)
+    q = c["q"].clone()
+    q[c["n"] // 2, 3] = bad
+    o, lse, ws = S.pa_paged_attend(q, *args)
+    assert ok(S, ws) == 0
+    keep = torch.ones(q.shape[:2], dtype=torch.bool, device="cuda")
+    keep[c["n"] // 2, 3] = False
+    assert torch.equal(o[keep], o0[keep]) and torch.equal(lse[keep], lse0[keep])
+    assert torch.isnan(o[c["n"] // 2, 3]).all()
+
+
+def test_scores_far_apart(S):
+    # scores of hundreds: the running maximum moves from tile to tile, most
+    # probabilities underflow, and nothing overflows
+    for dt in DTYPES.values():
+        for q_lens, kv_lens in (([1, 2], [900, 500]), ([130], [700])):
+            c = paged_batch(q_lens, kv_lens, 4, 2, 64, 16, dt, seed=22)
+            q = c["q"] * 40
+            o, lse, ws = S.pa_paged_attend(q, c["cu_q"], c["kv_len"], c["table"], c["k_pages"], c["v_pages"], c["max_q"])
+            assert ok(S, ws) == 0
+            check_paged(dict(c, q=q), o, lse, "far apart")
+
+
+def test_empty_calls(S):
+    t = torch.zeros((0, 4), dtype=torch.int32, device="cuda")
+    none = i32(np.zeros(0))
+    cu, kv, pos, slots, used, ws = S.pa_paged_schedule(none, none, t, none, 16, 3)
+    assert ok(S, ws) == 0 and cu.tolist() == [0] and slots.tolist() == [-1] * 3 and pos.tolist() == [0] * 3
+    assert used.tolist() == [0] and kv.numel() == 0
+    k = torch.zeros((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    kp = torch.zeros((1, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q, ko, ws = S.pa_paged_append(torch.zeros((0, 4, 64), dtype=torch.bfloat16, device="cuda"), k, k, none, none, kp, kp,
+                                  rope_theta=1e4, want_k=True)
+    assert q.shape == (0, 4, 64) and ko.shape == (0, 2, 64) and ok(S, ws) == 0
+    o, lse, ws = S.pa_paged_attend(q, i32([0, 0]), i32([5]), i32([[0]]), kp, kp, 1)
+    assert o.shape == (0, 4, 64) and ok(S, ws) == 0
+    # a cache without pages: every key reads as zero, and is recorded
+    q = torch.ones((1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    no = torch.zeros((0, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    for m in (1, 5):
+        q = torch.ones((m, 4, 64), dtype=torch.bfloat16, device="cuda")
+        o, lse, ws = S.pa_paged_attend(q, i32([0, m]), i32([m]), i32([[0]]), no, no, m)
+        assert ok(S, ws) == -1 and (o == 0).all()
+
+
 def test_calls_on_two_streams_and_repeated(S):
     # the same inputs give the same bits, on any stream, with a fresh or a used workspace
     c = paged_batch([1, 40, 1], [3000, 900, 20], 8, 2, 128, 16, torch.bfloat16, seed=7)
@@ -580,3 +651,16 @@ def test_outputs_stay_inside_their_buffers(S):
         assert (big_o[:32] == 99).all() and (big_o[32 + rows:] == 99).all()
         assert (big_l[:32] == 99).all() and (big_l[32 + rows:] == 99).all()
         assert (big_l[32:32 + rows] != 99).all()
+
+
+@pytest.mark.parametrize("case", [([1, 1], [700, 90]), ([40, 150], [300, 150])], ids=["decode", "tiles"])
+def test_stalled_barrier_times_out_and_context_survives(S, case):
+    import time
+    c = paged_batch(*case, 8, 2, 128, 16, torch.bfloat16, seed=15, poison=False)
+    args = (c["q"], c["cu_q"], c["kv_len"], c["table"], c["k_pages"], c["v_pages"], c["max_q"])
+    t0 = time.time()
+    assert ok(S, S.pa_testing_paged_stall(*args, wait_limit_us=20000)) == -5     # PA_ERR_TIMEOUT
+    assert time.time() - t0 < 30.0
+    o, lse, ws = S.pa_paged_attend(*args)
+    assert ok(S, ws) == 0
+    check_paged(c, o, lse, "after the stall")

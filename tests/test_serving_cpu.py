@@ -127,6 +127,7 @@ def test_binding_refuses_mismatched_tensors(S, monkeypatch):
     bad("o:", pr, q, k, k, cu, o=torch.zeros((10, 8, 64)))
     bad("o:", pr, q, k, k, cu, o=q[:9].clone())
     bad("lse:", pr, q, k, k, cu, lse=torch.zeros((10, 7)))
+    bad("must not be q", pr, q, k, k, cu, o=q)
     bad("kv_len", pg, q, cu, kv[:1], table, kp, kp, 1)
     bad("block_table", pg, q, cu, kv, table[:1], kp, kp, 1)
     bad("block_table", pg, q, cu, kv, table.long(), kp, kp, 1)
