@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(256, 2) attend_simt_kernel(AttendArgs a) {
       for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
     // (before the stores below: a tile that every row sees in full needs no mask)
     const bool whole = c0 + kKeys - 1 <= lim_first;
+    float alpha[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       float mt = m_run[i];
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(256, 2) attend_simt_kernel(AttendArgs a) {
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
       const float sub = mt == -INFINITY ? 0.f : mt;   // a row without a visible key so far
-      const float alpha = fast_exp2(m_run[i] - sub);
+      alpha[i] = fast_exp2(m_run[i] - sub);
       m_run[i] = mt;
       float sum = 0.f;
 #pragma unroll
@@ -179,14 +180,16 @@ __global__ void __launch_bounds__(256, 2) attend_simt_kernel(AttendArgs a) {
       }
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l_run[i] = l_run[i] * alpha + sum;
-#pragma unroll
-      for (int j = 0; j < 2 * CV; ++j) {
-        acc[i][j].x *= alpha;
-        acc[i][j].y *= alpha;
-      }
+      l_run[i] = l_run[i] * alpha[i] + sum;
     }
     __syncwarp();   // a row's 16 threads are in one warp
+    // each tile is summed by itself and then added: over thousands of keys the
+    // rounding of one long chain of sums would be several times larger
+    float2 part[R][2 * CV];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 2 * CV; ++j) part[i][j] = make_float2(0.f, 0.f);
     if (whole) {
 #pragma unroll 2
       for (int key = 0; key < kKeys; key += 4) {
@@ -202,8 +205,8 @@ __global__ void __launch_bounds__(256, 2) attend_simt_kernel(AttendArgs a) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
               const float2 pp = make_float2(p[i][k], p[i][k]);
-              acc[i][2 * j] = fma2(pp, make_float2(v4.x, v4.y), acc[i][2 * j]);
-              acc[i][2 * j + 1] = fma2(pp, make_float2(v4.z, v4.w), acc[i][2 * j + 1]);
+              part[i][2 * j] = fma2(pp, make_float2(v4.x, v4.y), part[i][2 * j]);
+              part[i][2 * j + 1] = fma2(pp, make_float2(v4.z, v4.w), part[i][2 * j + 1]);
             }
           }
       }
@@ -220,12 +223,16 @@ __global__ void __launch_bounds__(256, 2) attend_simt_kernel(AttendArgs a) {
             if (c0 + key <= lim[i]) {
               const float p = sp[(ty * R + i) * C::LDP + key];
               const float2 pp = make_float2(p, p);
-              acc[i][2 * j] = fma2(pp, make_float2(v4.x, v4.y), acc[i][2 * j]);
-              acc[i][2 * j + 1] = fma2(pp, make_float2(v4.z, v4.w), acc[i][2 * j + 1]);
+              part[i][2 * j] = fma2(pp, make_float2(v4.x, v4.y), part[i][2 * j]);
+              part[i][2 * j + 1] = fma2(pp, make_float2(v4.z, v4.w), part[i][2 * j + 1]);
             }
         }
       }
     }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 2 * CV; ++j) acc[i][j] = fma2(acc[i][j], make_float2(alpha[i], alpha[i]), part[i][j]);
     __syncthreads();   // the stage and its slots are refilled
   }
   asm volatile("cp.async.wait_group 0;\n" ::: "memory");
