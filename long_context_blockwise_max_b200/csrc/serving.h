@@ -243,7 +243,8 @@ __device__ __forceinline__ void block_incl_scan2(T& x, T& y, T* tmp, T* x_all, T
   __syncthreads();
   const T wx = warp_incl_scan(lane < warps ? tmp[lane] : T(0));
   const T wy = warp_incl_scan(lane < warps ? tmp[32 + lane] : T(0));
-  const T bx = __shfl_sync(0xffffffffu, wx, warp > 0 ? warp - 1 : 0), by = __shfl_sync(0xffffffffu, wy, warp > 0 ? warp - 1 : 0);
+  const int before = warp > 0 ? warp - 1 : 0;
+  const T bx = __shfl_sync(0xffffffffu, wx, before), by = __shfl_sync(0xffffffffu, wy, before);
   *x_all = __shfl_sync(0xffffffffu, wx, 31);
   *y_all = __shfl_sync(0xffffffffu, wy, 31);
   if (warp > 0) {

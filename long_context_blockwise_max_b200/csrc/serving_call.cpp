@@ -86,7 +86,8 @@ struct Args {
     return x;
   }
   Tensor make(at::IntArrayRef size, at::ScalarType type) const {
-    return at::detail::empty_cuda(size, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
+    const c10::Device device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev));
+    return at::detail::empty_cuda(size, type, device, std::nullopt);
   }
   void* stream() const { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
 };

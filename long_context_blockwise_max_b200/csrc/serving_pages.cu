@@ -114,8 +114,11 @@ __global__ void __launch_bounds__(1024) paged_schedule_kernel(ScheduleArgs a) {
 template <typename T>
 __global__ void __launch_bounds__(256) paged_append_kernel(AppendArgs a, RopeFreqs turns, int tpb) {
   constexpr int V = 16 / sizeof(T);            // elements per access
-  extern __shared__ float2 cs[];               // [tpb][d / 2] (cos, sin)
-  const int half = a.d / 2;
+  // (cos, sin) of angle m of token t at [t][m % V][m / V]: the threads of a head
+  // read neighbours ([t][m] cost four times the shared-memory cycles, and bound
+  // the kernel)
+  extern __shared__ float2 cs[];
+  const int half = a.d / 2, cpr = half / V;    // cpr: accesses per half row
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tpb;
   const int nt = static_cast<int>(min(static_cast<int64_t>(tpb), a.N - t0));
   const bool rope = a.rope_theta != 0.0;
@@ -133,11 +136,11 @@ __global__ void __launch_bounds__(256) paged_append_kernel(AppendArgs a, RopeFre
       const float f = static_cast<float>(x - rint(x));                       // in [-1/2, 1/2]
       float sn, cn;
       sincospif(2.f * f, &sn, &cn);
-      cs[e] = make_float2(cn, sn);
+      const int m = e % half;
+      cs[e - m + (m % V) * cpr + m / V] = make_float2(cn, sn);
     }
     __syncthreads();
   }
-  const int cpr = half / V;                    // accesses per half row
   const int hq = a.q ? a.hq : 0;
   const int hv = a.slots ? a.hkv : 0;
   const int per_tok = (hq + a.hkv + hv) * cpr;
@@ -171,12 +174,13 @@ __global__ void __launch_bounds__(256) paged_append_kernel(AppendArgs a, RopeFre
     *reinterpret_cast<uint4*>(x1) = *reinterpret_cast<const uint4*>(src + m);
     *reinterpret_cast<uint4*>(x2) = *reinterpret_cast<const uint4*>(src + m + half);
     if (rope && head < hq + a.hkv) {
-      const float2* c = cs + t * half + m;
+      const float2* c = cs + t * half + m / V;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float y1 = to_f32(x1[j]), y2 = to_f32(x2[j]);
-        x1[j] = from_f32<T>(y1 * c[j].x - y2 * c[j].y);
-        x2[j] = from_f32<T>(y2 * c[j].x + y1 * c[j].y);
+        const float2 r = c[j * cpr];
+        x1[j] = from_f32<T>(y1 * r.x - y2 * r.y);
+        x2[j] = from_f32<T>(y2 * r.x + y1 * r.y);
       }
     }
     if (dst) {

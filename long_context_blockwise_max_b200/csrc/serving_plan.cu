@@ -235,7 +235,9 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
       __syncthreads();
       // the longest first, by a counting sort (no piece is longer than `chunk`)
       const bool sort = static_cast<int64_t>(n_pieces) * a.hkv > a.slots;
-      auto bucket = [&](int d) { return kBuckets - 1 - static_cast<int>(static_cast<int64_t>(d) * (kBuckets - 1) / chunk); };
+      auto bucket = [&](int d) {
+        return kBuckets - 1 - static_cast<int>(static_cast<int64_t>(d) * (kBuckets - 1) / chunk);
+      };
       auto piece_len = [&](int x, int& i, int& kt0) {
         i = upper_index(first_piece, n + 1, x);
         const int p = first_piece[i + 1] - first_piece[i], k = x - first_piece[i];
@@ -260,7 +262,8 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
         const int len = piece_len(x, i, kt0);
         const int b = upper_index(items, a.B + 1, i);
         put_piece(a, sort ? atomicAdd(&hist[bucket(len)], 1) : x, b, lens_of(a, b, max_kv, false),
-                  (i - items[b]) * a.tile_tokens, kt0, kt0 + len, part_of[i] < 0 ? -1 : part_of[i] + x - first_piece[i]);
+                  (i - items[b]) * a.tile_tokens, kt0, kt0 + len,
+                  part_of[i] < 0 ? -1 : part_of[i] + x - first_piece[i]);
       }
     } else {
       // deepest first: a counting sort by depth (the order inside a bucket is
@@ -298,8 +301,8 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     a.head->n_items = n_merge;
     a.head->abort = 0;
     a.head->next = 0;
-    a.head->heads_inner = static_cast<double>(key_tiles) * kPlanTile * a.hkv * a.d * (a.dtype == PA_BF16 ? 4 : 8) <= kL2Keys ||
-                           n_pieces <= 2 * a.slots;
+    const double kv_bytes = static_cast<double>(key_tiles) * kPlanTile * a.hkv * a.d * (a.dtype == PA_BF16 ? 4 : 8);
+    a.head->heads_inner = kv_bytes <= kL2Keys || n_pieces <= 2 * a.slots;
   }
 }
 

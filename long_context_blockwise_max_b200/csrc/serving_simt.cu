@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(256, 2) attend_simt_kernel(AttendArgs a) {
 #pragma unroll
     for (int j = 0; j < CV; ++j)
       *reinterpret_cast<float4*>(dst + 64 * j + 4 * tx) =
-          make_float4(acc[i][2 * j].x * inv, acc[i][2 * j].y * inv, acc[i][2 * j + 1].x * inv, acc[i][2 * j + 1].y * inv);
+          make_float4(acc[i][2 * j].x * inv, acc[i][2 * j].y * inv, acc[i][2 * j + 1].x * inv,
+                      acc[i][2 * j + 1].y * inv);
     if (tx == 0) {
       if (pc.part >= 0) a.part_lse[part] = lse;
       else if (a.lse) a.lse[row] = lse;

@@ -61,7 +61,8 @@ struct SvCfg {
   static constexpr int OFF_OUT = OFF_V + 2 * TILE_BYTES;   // output staging, 2 KB per softmax warp
   static constexpr int OFF_BAR = OFF_OUT + 8 * 2048;
   static constexpr int SMEM_BYTES = OFF_BAR + 13 * 1024;
-  static constexpr float SCALE = static_cast<float>(kLog2e / (D == 128 ? 11.31370849898476039 : 8.0));  // log2(e) / sqrt(d)
+  // log2(e) / sqrt(d)
+  static constexpr float SCALE = static_cast<float>(kLog2e / (D == 128 ? 11.31370849898476039 : 8.0));
   static constexpr uint32_t IDESC_QK = idesc_f16(128, 128, 1, 1, 0, 0);  // bf16 Q . bf16 K
   static constexpr uint32_t IDESC_PV = idesc_f16(128, D, 1, 1, 0, 1);    // bf16 P . bf16 V (MN-major)
 };
@@ -140,7 +141,8 @@ __device__ void guard_tile(uint8_t* v, int first_row, int n_keys, int key0, int 
         if ((e[k] & 0x7f80) == 0x7f80) {
           const int kind = (e[k] & 0x7f) ? 2 : (e[k] >> 15);
           atomicMin(&bars->first[piece & 1][kind][8 * c + k],
-                    (static_cast<unsigned long long>(~static_cast<uint32_t>(piece + 1)) << 32) | static_cast<uint32_t>(key0 + r));
+                    (static_cast<unsigned long long>(~static_cast<uint32_t>(piece + 1)) << 32) |
+                        static_cast<uint32_t>(key0 + r));
           e[k] = 0;
         }
       *p = x;
@@ -278,8 +280,8 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
         if (!get_item(bars, k, it)) break;
         const int tok_t = it.tok0 + (it.two ? t * tpt : 0);   // first token of this warpgroup's rows
         const bool valid = rl < tpt * g && tok_t + rt < it.q_len;
-        lim = valid ? it.ctx + tok_t + rt : it.kv_len - 1;                         // last visible key
-        lim_w = it.ctx + tok_t + static_cast<int>((sub * 32 * ginv) >> 16);           // the smallest of this warp's rows
+        lim = valid ? it.ctx + tok_t + rt : it.kv_len - 1;                   // last visible key
+        lim_w = it.ctx + tok_t + static_cast<int>((sub * 32 * ginv) >> 16);   // the smallest of this warp's rows
         my = t == 0 ? it.nt0 : it.nt1;
         key_first = (it.kt0 + (it.two ? 0 : t)) * kKeyTile;
         key_step = it.two ? kKeyTile : 2 * kKeyTile;
@@ -395,7 +397,8 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       w_own *= inv;
       w_oth *= inv;
       const bool odd = *reinterpret_cast<volatile int*>(&bars->odd[k & 1]) == k + 1;
-      const int64_t prow = (static_cast<int64_t>(it.part) * a.hkv + it.kvh) * a.tile_rows + (two ? t * tpt * g : 0) + rl;
+      const int64_t prow =
+          (static_cast<int64_t>(it.part) * a.hkv + it.kvh) * a.tile_rows + (two ? t * tpt * g : 0) + rl;
       const int rows = min(tpt, it.q_len - tok_t) * g;     // rows of this tile
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) +
                            ((static_cast<int64_t>(it.row0) + tok_t) * a.hq + it.kvh * g) * D;
@@ -473,245 +476,247 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
     if (!ok) fail(9);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    const int nbox = kKeyTile / p.box_rows;
-    const int q_bytes = tpt * g * 128 * C::NKB;
-    uint32_t tile = 0;                  // K and V tiles before this one
-    uint32_t n_q = 0, n_k = 0;          // copies issued: Q's and K tiles,
-    uint32_t n_v0 = 0, n_v1 = 0, n_g0 = 0, n_g1 = 0;   // V tiles of each stage, guarded ones
-    // Units of work: this block's first, then whichever comes next over all
-    // blocks (the deepest come first, so the blocks end together).
-    const unsigned total = static_cast<unsigned>(a.head->n_pieces) * static_cast<unsigned>(a.hkv);
-    unsigned unit = blockIdx.x;
-    int at = 0, kvh = -1;
-    Piece after = {};                   // the piece after the current one
-    auto fetch = [&]() {
-      kvh = -1;
-      if (unit < total) {
-        piece_at(a, unit, &at, &kvh);
-        const int4 x = reinterpret_cast<const int4*>(a.pieces + at)[0], y = reinterpret_cast<const int4*>(a.pieces + at)[1];
-        after = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      }
-    };
-    fetch();
-    bool ok = true;
-    Item it;
-    for (int k = 0; ok; ++k) {
-      // the slot's previous piece (two before) is finished
-      if (k >= 2 && !wait(&bars->done[k & 1], (k >> 1) - 1)) { ok = false; break; }
-      if (lane == 0) {
-        put_item(bars, k, tpt, after, kvh);
-        mbar_arrive(&bars->work_full[k & 1]);
-      }
-      __syncwarp();
-      if (!get_item(bars, k, it)) break;
-      // row coordinate of this lane's box of tile j
-      auto row_of = [&](int j) -> int {
-        if (!PAGED) return it.row0 + j * kKeyTile;
-        const int64_t key = static_cast<int64_t>(j) * kKeyTile + lane * p.box_rows;
-        if (lane >= nbox || key >= it.kv_len) return p.oob_row;
-        const int64_t slot = key_slot(a, it.b, key);
-        return slot < 0 ? p.oob_row : static_cast<int>(slot);
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      const int nbox = kKeyTile / p.box_rows;
+      const int q_bytes = tpt * g * 128 * C::NKB;
+      uint32_t tile = 0;                  // K and V tiles before this one
+      uint32_t n_q = 0, n_k = 0;          // copies issued: Q's and K tiles,
+      uint32_t n_v0 = 0, n_v1 = 0, n_g0 = 0, n_g1 = 0;   // V tiles of each stage, guarded ones
+      // Units of work: this block's first, then whichever comes next over all
+      // blocks (the deepest come first, so the blocks end together).
+      const unsigned total = static_cast<unsigned>(a.head->n_pieces) * static_cast<unsigned>(a.hkv);
+      unsigned unit = blockIdx.x;
+      int at = 0, kvh = -1;
+      Piece after = {};                   // the piece after the current one
+      auto fetch = [&]() {
+        kvh = -1;
+        if (unit < total) {
+          piece_at(a, unit, &at, &kvh);
+          const int4* src = reinterpret_cast<const int4*>(a.pieces + at);
+          const int4 x = src[0], y = src[1];
+          after = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        }
       };
-      int row = it.n > 0 ? row_of(it.kt0) : 0;
-      if (k > 0 && !wait(&bars->q_empty, k - 1)) { ok = false; break; }
-      if (lane == 0) {
-        const int qt = it.two ? 2 : 1;
-        mbar_arrive_expect_tx(&bars->q_full, qt * q_bytes + (a.stall ? 16 : 0));
-        for (int t = 0; t < qt; ++t)
-          for (int kb = 0; kb < C::NKB; ++kb)
-            tma_load_3d(sQ + t * C::TILE_BYTES + kb * C::KB_BYTES, &tmQ, &bars->q_full, kb * 64, it.kvh * g,
-                        it.row0 + it.tok0 + t * tpt);
-      }
-      ++n_q;
-      for (int jj = 0; jj < it.n; ++jj, ++tile) {
-        const int st = tile & 1;
-        const uint32_t ph = tile >> 1;
-        const int next = jj + 1 < it.n ? row_of(it.kt0 + jj + 1) : 0;
-        if (!wait(&bars->k_empty[st], ph + 1)) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], C::TILE_BYTES);
-        __syncwarp();
-        if (lane < nbox)
-          for (int kb = 0; kb < C::NKB; ++kb)
-            tma_load_3d(sK + st * C::TILE_BYTES + kb * C::KB_BYTES + lane * p.box_rows * 128, &tmK,
-                        &bars->k_full[st], kb * 64, it.kvh, row);
-        ++n_k;
-        if (!wait(&bars->v_empty[st], ph + 1)) { ok = false; break; }
-        const bool guarded = jj >= it.g0;
-        uint64_t* full = guarded ? &bars->vg_full[st] : &bars->v_full[st];
-        if (lane == 0) mbar_arrive_expect_tx(full, C::TILE_BYTES);
-        __syncwarp();
-        if (lane < nbox)
-          for (int kb = 0; kb < C::NKB; ++kb)
-            tma_load_3d(sV + st * C::TILE_BYTES + kb * C::KB_BYTES + lane * p.box_rows * 128, &tmV, full, kb * 64,
-                        it.kvh, row);
-        n_v0 += !guarded && st == 0;
-        n_v1 += !guarded && st == 1;
-        n_g0 += guarded && st == 0;
-        n_g1 += guarded && st == 1;
-        row = next;
-      }
-      // (not before: a unit taken early would wait here while other blocks run out of work)
-      if (lane == 0) unit = gridDim.x + atomicAdd(&a.head->next, 1u);
-      unit = __shfl_sync(0xffffffffu, unit, 0);
       fetch();
-    }
-    if (lane == 0) {
-      if (!ok) fail(1);
-      // Drain: every copy this warp started has landed before the block ends.
-      int zero = 0;
-      auto landed = [&](uint64_t* bar, uint32_t count) {
-        if (count > 0) mbar_wait(bar, (count - 1) & 1, &zero, a.wait_limit_ns);
-      };
-      landed(&bars->q_full, n_q);
-      landed(&bars->k_full[0], (n_k + 1) >> 1);
-      landed(&bars->k_full[1], n_k >> 1);
-      landed(&bars->v_full[0], n_v0);
-      landed(&bars->v_full[1], n_v1);
-      landed(&bars->vg_full[0], n_g0);
-      landed(&bars->vg_full[1], n_g1);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
-      const uint64_t v_desc = sdesc_sw128(smem_u32(sV), C::KB_BYTES, 1024);
-      // scores of warpgroup t from row tile qt
-      auto qk = [&](int t, int qt, int st) {
-        const uint32_t d_tmem = tmem + t * 256;
-        const uint64_t qd = sdesc_add(q_desc, qt * C::TILE_BYTES);
-        const uint64_t kd = sdesc_add(k_desc, st * C::TILE_BYTES);
-#pragma unroll
-        for (int kb = 0; kb < C::NKB; ++kb)
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_ss(d_tmem, sdesc_add(qd, kb * C::KB_BYTES + ks * 32), sdesc_add(kd, kb * C::KB_BYTES + ks * 32),
-                   C::IDESC_QK, (kb | ks) != 0);
-        mma_commit(&bars->s_full[t]);
-      };
-      auto pv = [&](int t, int st, int acc) {
-        const uint32_t d_tmem = tmem + t * 256 + 128;
-        const uint64_t vd = sdesc_add(v_desc, st * C::TILE_BYTES);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ts(d_tmem, tmem + t * 256 + ks * 8, sdesc_add(vd, ks * 2048), C::IDESC_PV, (acc | ks) != 0);
-      };
-      uint32_t tile = 0;                        // K and V tiles before this piece
-      // phases, one bit each: of each warpgroup's P, and of each stage's V
-      // tiles and guarded V tiles
-      uint32_t ph_p = 0, ph_v = 0, ph_g = 0;
-      auto next = [](uint32_t& bits, int i) {
-        const uint32_t b = (bits >> i) & 1;
-        bits ^= 1u << i;
-        return b;
-      };
-      auto wait_k = [&](uint32_t x) { return wait_one(&bars->k_full[x & 1], x >> 1); };
       bool ok = true;
       Item it;
-      for (int k = 0; ok; ++k, tile += it.n) {
-        if (!wait_one(&bars->work_full[k & 1], k >> 1)) { fail(2); break; }
+      for (int k = 0; ok; ++k) {
+        // the slot's previous piece (two before) is finished
+        if (k >= 2 && !wait(&bars->done[k & 1], (k >> 1) - 1)) { ok = false; break; }
+        if (lane == 0) {
+          put_item(bars, k, tpt, after, kvh);
+          mbar_arrive(&bars->work_full[k & 1]);
+        }
+        __syncwarp();
         if (!get_item(bars, k, it)) break;
-        const int n = it.n;
-        auto wait_v = [&](int jj) {
-          const int st = (tile + jj) & 1;
-          return jj < it.g0 ? wait_one(&bars->v_full[st], next(ph_v, st)) : wait_one(&bars->v_ready[st], next(ph_g, st));
+        // row coordinate of this lane's box of tile j
+        auto row_of = [&](int j) -> int {
+          if (!PAGED) return it.row0 + j * kKeyTile;
+          const int64_t key = static_cast<int64_t>(j) * kKeyTile + lane * p.box_rows;
+          if (lane >= nbox || key >= it.kv_len) return p.oob_row;
+          const int64_t slot = key_slot(a, it.b, key);
+          return slot < 0 ? p.oob_row : static_cast<int>(slot);
         };
-        // the previous piece's O has been read before the first P V of this one
-        auto wait_o = [&]() { return k == 0 || wait_one(&bars->done[(k - 1) & 1], (k - 1) >> 1); };
-        if (!wait_one(&bars->q_full, k)) { fail(3); break; }
-        if (n == 0) {
-          mma_commit(&bars->q_empty);
-        } else if (it.two) {
-          if (!wait_k(tile)) { fail(4); break; }
-          tc_fence_after();
-          if (it.nt0 > 0) qk(0, 0, tile & 1);
-          qk(1, 1, tile & 1);
-          mma_commit(&bars->k_empty[tile & 1]);
-          if (n == 1) mma_commit(&bars->q_empty);
-          for (int jj = 0; ok && jj < n; ++jj) {
-            const int st = (tile + jj) & 1, st1 = st ^ 1;
-            // V_j and K_{j+1} first, while the tensor pipe still runs the other
-            // tile's MMAs, so that nothing stands between P and its products
-            if (!wait_v(jj)) { fail(6); ok = false; break; }
-            if (jj + 1 < n && !wait_k(tile + jj + 1)) { fail(7); ok = false; break; }
-            if (jj == 0 && !wait_o()) { fail(12); ok = false; break; }
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const int nt = t == 0 ? it.nt0 : n;
-              if (jj < nt) {
-                if (!wait_one(&bars->p_full[t], next(ph_p, t))) { fail(5); ok = false; break; }
-                tc_fence_after();
-                pv(t, st, jj > 0);
-                if (jj == nt - 1) mma_commit(&bars->o_final[t]);
+        int row = it.n > 0 ? row_of(it.kt0) : 0;
+        if (k > 0 && !wait(&bars->q_empty, k - 1)) { ok = false; break; }
+        if (lane == 0) {
+          const int qt = it.two ? 2 : 1;
+          mbar_arrive_expect_tx(&bars->q_full, qt * q_bytes + (a.stall ? 16 : 0));
+          for (int t = 0; t < qt; ++t)
+            for (int kb = 0; kb < C::NKB; ++kb)
+              tma_load_3d(sQ + t * C::TILE_BYTES + kb * C::KB_BYTES, &tmQ, &bars->q_full, kb * 64, it.kvh * g,
+                          it.row0 + it.tok0 + t * tpt);
+        }
+        ++n_q;
+        for (int jj = 0; jj < it.n; ++jj, ++tile) {
+          const int st = tile & 1;
+          const uint32_t ph = tile >> 1;
+          const int next = jj + 1 < it.n ? row_of(it.kt0 + jj + 1) : 0;
+          if (!wait(&bars->k_empty[st], ph + 1)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], C::TILE_BYTES);
+          __syncwarp();
+          if (lane < nbox)
+            for (int kb = 0; kb < C::NKB; ++kb)
+              tma_load_3d(sK + st * C::TILE_BYTES + kb * C::KB_BYTES + lane * p.box_rows * 128, &tmK,
+                          &bars->k_full[st], kb * 64, it.kvh, row);
+          ++n_k;
+          if (!wait(&bars->v_empty[st], ph + 1)) { ok = false; break; }
+          const bool guarded = jj >= it.g0;
+          uint64_t* full = guarded ? &bars->vg_full[st] : &bars->v_full[st];
+          if (lane == 0) mbar_arrive_expect_tx(full, C::TILE_BYTES);
+          __syncwarp();
+          if (lane < nbox)
+            for (int kb = 0; kb < C::NKB; ++kb)
+              tma_load_3d(sV + st * C::TILE_BYTES + kb * C::KB_BYTES + lane * p.box_rows * 128, &tmV, full, kb * 64,
+                          it.kvh, row);
+          n_v0 += !guarded && st == 0;
+          n_v1 += !guarded && st == 1;
+          n_g0 += guarded && st == 0;
+          n_g1 += guarded && st == 1;
+          row = next;
+        }
+        // (not before: a unit taken early would wait here while other blocks run out of work)
+        if (lane == 0) unit = gridDim.x + atomicAdd(&a.head->next, 1u);
+        unit = __shfl_sync(0xffffffffu, unit, 0);
+        fetch();
+      }
+      if (lane == 0) {
+        if (!ok) fail(1);
+        // Drain: every copy this warp started has landed before the block ends.
+        int zero = 0;
+        auto landed = [&](uint64_t* bar, uint32_t count) {
+          if (count > 0) mbar_wait(bar, (count - 1) & 1, &zero, a.wait_limit_ns);
+        };
+        landed(&bars->q_full, n_q);
+        landed(&bars->k_full[0], (n_k + 1) >> 1);
+        landed(&bars->k_full[1], n_k >> 1);
+        landed(&bars->v_full[0], n_v0);
+        landed(&bars->v_full[1], n_v1);
+        landed(&bars->vg_full[0], n_g0);
+        landed(&bars->vg_full[1], n_g1);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issue
+      if (lane == 0) {
+        const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t v_desc = sdesc_sw128(smem_u32(sV), C::KB_BYTES, 1024);
+        // scores of warpgroup t from row tile qt
+        auto qk = [&](int t, int qt, int st) {
+          const uint32_t d_tmem = tmem + t * 256;
+          const uint64_t qd = sdesc_add(q_desc, qt * C::TILE_BYTES);
+          const uint64_t kd = sdesc_add(k_desc, st * C::TILE_BYTES);
+  #pragma unroll
+          for (int kb = 0; kb < C::NKB; ++kb)
+  #pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ss(d_tmem, sdesc_add(qd, kb * C::KB_BYTES + ks * 32), sdesc_add(kd, kb * C::KB_BYTES + ks * 32),
+                     C::IDESC_QK, (kb | ks) != 0);
+          mma_commit(&bars->s_full[t]);
+        };
+        auto pv = [&](int t, int st, int acc) {
+          const uint32_t d_tmem = tmem + t * 256 + 128;
+          const uint64_t vd = sdesc_add(v_desc, st * C::TILE_BYTES);
+  #pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ts(d_tmem, tmem + t * 256 + ks * 8, sdesc_add(vd, ks * 2048), C::IDESC_PV, (acc | ks) != 0);
+        };
+        uint32_t tile = 0;                        // K and V tiles before this piece
+        // phases, one bit each: of each warpgroup's P, and of each stage's V
+        // tiles and guarded V tiles
+        uint32_t ph_p = 0, ph_v = 0, ph_g = 0;
+        auto next = [](uint32_t& bits, int i) {
+          const uint32_t b = (bits >> i) & 1;
+          bits ^= 1u << i;
+          return b;
+        };
+        auto wait_k = [&](uint32_t x) { return wait_one(&bars->k_full[x & 1], x >> 1); };
+        bool ok = true;
+        Item it;
+        for (int k = 0; ok; ++k, tile += it.n) {
+          if (!wait_one(&bars->work_full[k & 1], k >> 1)) { fail(2); break; }
+          if (!get_item(bars, k, it)) break;
+          const int n = it.n;
+          auto wait_v = [&](int jj) {
+            const int st = (tile + jj) & 1;
+            return jj < it.g0 ? wait_one(&bars->v_full[st], next(ph_v, st))
+                              : wait_one(&bars->v_ready[st], next(ph_g, st));
+          };
+          // the previous piece's O has been read before the first P V of this one
+          auto wait_o = [&]() { return k == 0 || wait_one(&bars->done[(k - 1) & 1], (k - 1) >> 1); };
+          if (!wait_one(&bars->q_full, k)) { fail(3); break; }
+          if (n == 0) {
+            mma_commit(&bars->q_empty);
+          } else if (it.two) {
+            if (!wait_k(tile)) { fail(4); break; }
+            tc_fence_after();
+            if (it.nt0 > 0) qk(0, 0, tile & 1);
+            qk(1, 1, tile & 1);
+            mma_commit(&bars->k_empty[tile & 1]);
+            if (n == 1) mma_commit(&bars->q_empty);
+            for (int jj = 0; ok && jj < n; ++jj) {
+              const int st = (tile + jj) & 1, st1 = st ^ 1;
+              // V_j and K_{j+1} first, while the tensor pipe still runs the other
+              // tile's MMAs, so that nothing stands between P and its products
+              if (!wait_v(jj)) { fail(6); ok = false; break; }
+              if (jj + 1 < n && !wait_k(tile + jj + 1)) { fail(7); ok = false; break; }
+              if (jj == 0 && !wait_o()) { fail(12); ok = false; break; }
+  #pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const int nt = t == 0 ? it.nt0 : n;
+                if (jj < nt) {
+                  if (!wait_one(&bars->p_full[t], next(ph_p, t))) { fail(5); ok = false; break; }
+                  tc_fence_after();
+                  pv(t, st, jj > 0);
+                  if (jj == nt - 1) mma_commit(&bars->o_final[t]);
+                }
+                if (t == 1) mma_commit(&bars->v_empty[st]);
+                if (jj + 1 < nt) qk(t, t, st1);
               }
-              if (t == 1) mma_commit(&bars->v_empty[st]);
-              if (jj + 1 < nt) qk(t, t, st1);
+              if (ok && jj + 1 < n) {
+                mma_commit(&bars->k_empty[st1]);
+                if (jj + 2 == n) mma_commit(&bars->q_empty);
+              }
             }
-            if (ok && jj + 1 < n) {
-              mma_commit(&bars->k_empty[st1]);
-              if (jj + 2 == n) mma_commit(&bars->q_empty);
+          } else {
+            for (int jj = 0; jj < min(n, 2); ++jj) {
+              if (!wait_k(tile + jj)) { fail(4); ok = false; break; }
+              tc_fence_after();
+              qk(jj, 0, (tile + jj) & 1);
+              mma_commit(&bars->k_empty[(tile + jj) & 1]);
             }
-          }
-        } else {
-          for (int jj = 0; jj < min(n, 2); ++jj) {
-            if (!wait_k(tile + jj)) { fail(4); ok = false; break; }
-            tc_fence_after();
-            qk(jj, 0, (tile + jj) & 1);
-            mma_commit(&bars->k_empty[(tile + jj) & 1]);
-          }
-          if (!ok) break;
-          if (n <= 2) mma_commit(&bars->q_empty);
-          for (int jj = 0; jj < n; ++jj) {
-            const int t = jj & 1, i = jj >> 1, st = (tile + jj) & 1;
-            if (!wait_v(jj)) { fail(6); ok = false; break; }
-            if (jj + 2 < n && !wait_k(tile + jj + 2)) { fail(7); ok = false; break; }
-            if (jj == 0 && !wait_o()) { fail(12); ok = false; break; }
-            if (!wait_one(&bars->p_full[t], next(ph_p, t))) { fail(5); ok = false; break; }
-            tc_fence_after();
-            pv(t, st, i > 0);
-            if (jj + 2 >= n) mma_commit(&bars->o_final[t]);
-            mma_commit(&bars->v_empty[st]);
-            if (jj + 2 < n) {
-              qk(t, 0, st);
-              mma_commit(&bars->k_empty[st]);
-              if (jj + 3 == n) mma_commit(&bars->q_empty);
+            if (!ok) break;
+            if (n <= 2) mma_commit(&bars->q_empty);
+            for (int jj = 0; jj < n; ++jj) {
+              const int t = jj & 1, i = jj >> 1, st = (tile + jj) & 1;
+              if (!wait_v(jj)) { fail(6); ok = false; break; }
+              if (jj + 2 < n && !wait_k(tile + jj + 2)) { fail(7); ok = false; break; }
+              if (jj == 0 && !wait_o()) { fail(12); ok = false; break; }
+              if (!wait_one(&bars->p_full[t], next(ph_p, t))) { fail(5); ok = false; break; }
+              tc_fence_after();
+              pv(t, st, i > 0);
+              if (jj + 2 >= n) mma_commit(&bars->o_final[t]);
+              mma_commit(&bars->v_empty[st]);
+              if (jj + 2 < n) {
+                qk(t, 0, st);
+                mma_commit(&bars->k_empty[st]);
+                if (jj + 3 == n) mma_commit(&bars->q_empty);
+              }
             }
           }
         }
+        // Drain: all MMAs issued by this thread complete before TMEM is freed.
+        int zero = 0;
+        mma_commit(&bars->drain);
+        mbar_wait(&bars->drain, 0, &zero, a.wait_limit_ns);
       }
-      // Drain: all MMAs issued by this thread complete before TMEM is freed.
-      int zero = 0;
-      mma_commit(&bars->drain);
-      mbar_wait(&bars->drain, 0, &zero, a.wait_limit_ns);
-    }
-  } else if (warp < 4) {
-    // ---------------------------------------------------------- V guard
-    const int tid = threadIdx.x - 64;
-    uint32_t tile = 0, ph_g = 0;   // ph_g: phase bit of each stage's guarded tiles
-    bool ok = true;
-    Item it;
-    for (int k = 0; ok; ++k, tile += it.n) {
-      // (a piece is there only when the one two before, whose notes it takes over, is finished)
-      if (!wait(&bars->work_full[k & 1], k >> 1)) { ok = false; break; }
-      if (!get_item(bars, k, it)) break;
-      const int lim_first = it.ctx + it.tok0;
-      for (int jj = it.g0; jj < it.n; ++jj) {
-        const int st = (tile + jj) & 1;
-        if (!wait(&bars->vg_full[st], ph_g >> st)) { ok = false; break; }
-        ph_g ^= 1u << st;
-        const int key0 = (it.kt0 + jj) * kKeyTile;
-        guard_tile<D>(sV + st * C::TILE_BYTES, max(0, lim_first + 1 - key0), it.kv_len - key0, key0, k, bars, tid);
-        fence_async_smem();
+    } else if (warp < 4) {
+      // ---------------------------------------------------------- V guard
+      const int tid = threadIdx.x - 64;
+      uint32_t tile = 0, ph_g = 0;   // ph_g: phase bit of each stage's guarded tiles
+      bool ok = true;
+      Item it;
+      for (int k = 0; ok; ++k, tile += it.n) {
+        // (a piece is there only when the one two before, whose notes it takes over, is finished)
+        if (!wait(&bars->work_full[k & 1], k >> 1)) { ok = false; break; }
+        if (!get_item(bars, k, it)) break;
+        const int lim_first = it.ctx + it.tok0;
+        for (int jj = it.g0; jj < it.n; ++jj) {
+          const int st = (tile + jj) & 1;
+          if (!wait(&bars->vg_full[st], ph_g >> st)) { ok = false; break; }
+          ph_g ^= 1u << st;
+          const int key0 = (it.kt0 + jj) * kKeyTile;
+          guard_tile<D>(sV + st * C::TILE_BYTES, max(0, lim_first + 1 - key0), it.kv_len - key0, key0, k, bars, tid);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->v_ready[st]);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->v_ready[st]);
+        if (lane == 0) mbar_arrive(&bars->noted[k & 1]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->noted[k & 1]);
+      if (!ok && lane == 0) fail(11);
     }
-    if (!ok && lane == 0) fail(11);
-  }
   }
   tc_fence_before();
   __syncthreads();
@@ -741,7 +746,9 @@ int launch_tc(const AttendArgs& a, cudaStream_t s) {
     return PA_ERR_CUDA;
   const int rc = allow_smem<attend_tc_kernel<D, PAGED>>(C::SMEM_BYTES);
   if (rc != PA_OK) return rc;
-  return launch_overlapped(attend_tc_kernel<D, PAGED>, dim3(tile_blocks(a) < kSms ? tile_blocks(a) : kSms), 384, C::SMEM_BYTES, s, mq, mk, mv, p);
+  const unsigned units = tile_blocks(a);
+  return launch_overlapped(attend_tc_kernel<D, PAGED>, dim3(units < kSms ? units : kSms), 384, C::SMEM_BYTES, s, mq, mk,
+                           mv, p);
 }
 
 }  // namespace
@@ -761,9 +768,9 @@ bool rows_map(void* map, const void* base, int64_t rows, int heads, int d, int64
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(ld) * 2};
   cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[3] = {1, 1, 1};
-  return enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int launch_attend_tc(const AttendArgs& a, cudaStream_t s) {
