@@ -27,11 +27,13 @@
  *  - d is 64 or 128; hq % hkv == 0, hq / hkv <= 64; query head h reads kv head
  *    h / (hq / hkv).  B <= 8192, N < 2^31.
  *  - Lengths and tables are read on the device only, so a captured call may
- *    be replayed with other lengths that fit the same arguments.  Lengths
+ *    be replayed with other lengths that fit the same arguments.  Calls that
+ *    share a workspace, captured or not, must not overlap on the GPU.  Lengths
  *    out of range (a cu_q that falls or passes N, a negative kv_len or one
  *    above max_pages * page_size) set PA_ERR_INVALID in the workspace status
  *    and that request is skipped; a page outside [0, n_pages) sets it and
- *    its keys read as zeros.
+ *    its keys read as zeros.  Where a cu_q falls, requests may share rows:
+ *    which of them such a row is answered for is not defined.
  */
 #ifndef PULSAR_B200_SERVING_H
 #define PULSAR_B200_SERVING_H
@@ -95,6 +97,8 @@ size_t pa_paged_append_workspace_size(int64_t N);
  *                 is hq * d.
  *  k_out_opt      out [N][hkv][d] dense: the rotated k, or NULL.  May equal k
  *                 when ldk is hkv * d.
+ * q_out and k_out_opt are written for all N tokens, those without a slot
+ * included.
  * RoPE is rotate-half, omega_m = rope_theta^(-2m/d), the angle reduced in
  * fp64, the rotation in fp32, one rounding to dtype; rope_theta == 0: no
  * rotation.

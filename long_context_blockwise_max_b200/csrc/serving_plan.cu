@@ -151,9 +151,11 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
   // ---- tiles --------------------------------------------------------------
   int n_pieces = 0;
   if (a.tiles) {
-    const int64_t most = a.piece_cap;
+    // (offsets that fall and rise again count rows twice: what is above the
+    // most that N rows can make is dropped, and cutting adds at most part_cap)
+    const int64_t most = a.piece_cap - a.part_cap;
     const int n = static_cast<int>(item_base < most ? item_base : most);
-    if (item_base > most && tid == 0) set_status(a.status, PA_ERR_INVALID, a.B);   // rows counted twice
+    if (item_base > most && tid == 0) set_status(a.status, PA_ERR_INVALID, a.B);
     const int64_t blocks = static_cast<int64_t>(n) * a.hkv;
     bool cut = a.part_cap > 0 && n > 0 && blocks < 3 * a.slots && n <= kMaxCutItems && deepest > 1;
     int parts = 1;

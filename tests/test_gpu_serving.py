@@ -423,6 +423,35 @@ def test_scores_far_apart(S):
             check_paged(dict(c, q=q), o, lse, "far apart")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,n", [(31, 700), (8001, 64), (201, 3)])
+def test_offsets_that_count_rows_twice_stay_inside_the_workspace(S, dtype, B, n):
+    # cu_q = 0, n, 0, n, ...: every other request has all the rows, together far
+    # more than the call has; the rest falls and is recorded.  A second workspace
+    # behind the first one is left as it was, and a good call in the same one is right.
+    cu = torch.tensor([0, n] * ((B + 1) // 2), dtype=torch.int32, device="cuda")
+    q, k, v = randn((n, 8, 64), DTYPES[dtype], 1), randn((n, 2, 64), DTYPES[dtype], 2), randn((n, 2, 64), DTYPES[dtype], 3)
+    need = S._lib.pa_prompt_attend_workspace_size(B, n, 8, 2, 64, 1 if dtype == "bf16" else 0)
+    whole = torch.full((need + 65536,), 93, dtype=torch.uint8, device="cuda")
+    _, _, ws = S.pa_prompt_attend(q, k, v, cu, ws=whole[:need])
+    assert ok(S, ws) == -1 and (whole[need:] == 93).all()
+    kp, vp = randn((n // 16 + 1, 16, 2, 64), DTYPES[dtype], 4), randn((n // 16 + 1, 16, 2, 64), DTYPES[dtype], 5)
+    table = torch.arange(n // 16 + 1, dtype=torch.int32, device="cuda").repeat(B, 1)
+    kv = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    need = S._lib.pa_paged_attend_workspace_size(B, n, n, table.shape[1], 16, 8, 2, 64, 1 if dtype == "bf16" else 0)
+    whole = torch.full((need + 65536,), 93, dtype=torch.uint8, device="cuda")
+    _, _, ws = S.pa_paged_attend(q, cu, kv, table, kp, vp, n, ws=whole[:need])
+    assert ok(S, ws) == -1 and (whole[need:] == 93).all()
+    cu = torch.full((B + 1,), n, dtype=torch.int32, device="cuda")
+    cu[0] = 0
+    o, lse, ws = S.pa_paged_attend(q, cu, kv, table, kp, vp, n, ws=whole[:need])
+    assert ok(S, ws) == 0 and (whole[need:] == 93).all()
+    o1, lse1, _ = S.pa_paged_attend(q, cu[:2], kv[:1], table[:1], kp, vp, n)
+    # each answer: P rounded (half a step of |v|) and o rounded (half a step of |o| <= |v|)
+    tol = 4 * 2.0 ** -8 * float(vp.float().abs().max())
+    assert (o.float() - o1.float()).abs().max() <= tol and (lse - lse1).abs().max() <= 1e-4
+
+
 def test_empty_calls(S):
     t = torch.zeros((0, 4), dtype=torch.int32, device="cuda")
     none = i32(np.zeros(0))
