@@ -181,7 +181,7 @@ PyObject* paged_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int type = dtype_of(*k);
     if (!a.ok || type < 0 || q->scalar_type() != k->scalar_type() || v->scalar_type() != k->scalar_type() ||
         v->sizes() != k->sizes() || q->size(0) != N || q->size(2) != d || N > kMaxInt || hq > kMaxInt ||
-        !cache_ok(kp, vp, k->scalar_type(), d) || kp->size(2) != hkv)
+        !cache_ok(kp, vp, k->scalar_type(), d) || kp->size(2) != hkv || kp->data_ptr() == vp->data_ptr())
       return to_slow();
     Tensor q_out = a.make({N, hq, d}, q->scalar_type()), k_out, ws = a.make({256}, at::kByte);
     if (PyObject_IsTrue(args[8])) k_out = a.make({N, hkv, d}, k->scalar_type());

@@ -85,6 +85,24 @@ def _dense(*named):
             raise ValueError(f"{name}: must be contiguous")
 
 
+def _span(t):
+    """First and last byte address of a tensor's elements, or None."""
+    if t is None or t.numel() == 0:
+        return None
+    last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size() - 1
+
+
+def _apart(outs, ins):
+    """Outputs share no memory with inputs or with one another."""
+    for i, (name, out) in enumerate(outs):
+        o = _span(out)
+        for other, t in list(ins) + list(outs[i + 1:]):
+            x = _span(t)
+            if o and x and o[0] <= x[1] and x[0] <= o[1]:
+                raise ValueError(f"{name}: overlaps {other}")
+
+
 def _rows(t: torch.Tensor, name: str, d: int | None = None):
     """Packed [N][heads][d] rows, dense inside a token: the token stride."""
     if t.dim() != 3:
@@ -170,8 +188,9 @@ def pa_paged_schedule(q_len, kv_len, block_table, free_pages, page_size: int, n_
     _ints((("cu_q", cu_q),), B + 1)
     _ints((("positions", positions), ("slots", slots)), n_tokens)
     _ints((("n_used", n_used),), 1)
-    if kv_len_out is not None and kv_len_out.data_ptr() == kv_len.data_ptr() and B > 0:
-        raise ValueError("kv_len_out: must not be kv_len")
+    _apart([("kv_len_out", kv_len_out), ("cu_q", cu_q), ("positions", positions), ("slots", slots),
+            ("n_used", n_used), ("block_table", block_table)],
+           [("q_len", q_len), ("kv_len", kv_len), ("free_pages", free_pages)])
     given = (cu_q, kv_len_out, positions, slots, n_used)
     sizes = (B + 1, B, n_tokens, n_tokens, 1)
     if any(t is None for t in given):   # one allocation for those that are missing
@@ -239,10 +258,16 @@ def pa_paged_append(q, k_new, v_new, positions, slots, k_pages, v_pages, rope_th
     _need(k_out, "k_out", k_new.dtype, N * hkv * d)
     if q_out is not None or k_out is not None:
         _dense(("q_out", q_out), ("k_out", k_out))
+    ins = [("q", q), ("k_new", k_new), ("v_new", v_new), ("positions", positions), ("slots", slots)]
+    pages = [("k_pages", k_pages), ("v_pages", v_pages)]
     for name, out, src, ld in (("q_out", q_out, q, ldq), ("k_out", k_out, k_new, ldk)):
-        if out is not None and src is not None and out.data_ptr() == src.data_ptr() and N > 1 \
-                and ld != src.shape[1] * d:
+        here = out is not None and src is not None and out.data_ptr() == src.data_ptr()
+        if here and N > 1 and ld != src.shape[1] * d:
             raise ValueError(f"{name}: in place only for dense rows")
+        _apart([(name, out)], [i for i in ins if not (here and i[1] is src)] + pages)
+    _apart([("q_out", q_out), ("k_out", k_out)], ())
+    if N > 0:
+        _apart(pages, ins)
     if q is not None and q_out is None:
         q_out = torch.empty((N, hq, d), dtype=q.dtype, device=q.device)
     if k_out is None and want_k:
@@ -253,10 +278,12 @@ def pa_paged_append(q, k_new, v_new, positions, slots, k_pages, v_pages, rope_th
     return q_out, k_out, ws
 
 
-def _attend_outputs(q, o, lse, want_lse):
+def _attend_outputs(q, o, lse, want_lse, ins):
     N, hq, d = q.shape
     if o is not None and N > 0 and o.data_ptr() == q.data_ptr():
         raise ValueError("o: must not be q")
+    if o is not None or lse is not None:
+        _apart([("o", o), ("lse", lse)], ins)
     _need(o, "o", q.dtype, N * hq * d)
     _need(lse, "lse", torch.float32, N * hq)
     _dense(("o", o), ("lse", lse))
@@ -294,7 +321,7 @@ def pa_prompt_attend(q, k, v, cu_q, o=None, lse=None, want_lse: bool = True, ws=
     if k.shape[0] != N or k.dtype != q.dtype:
         raise ValueError(f"k: {k.dtype} {tuple(k.shape)} does not match q {q.dtype} {tuple(q.shape)}")
     hkv, B, dt = k.shape[1], _batch(cu_q), _dtype_code(q)
-    o, lse = _attend_outputs(q, o, lse, want_lse)
+    o, lse = _attend_outputs(q, o, lse, want_lse, [("q", q), ("k", k), ("v", v), ("cu_q", cu_q)])
     if ws is None:
         ws = _ws(pa_prompt_attend_workspace_size(B, N, hq, hkv, d, dt), q, None)
     ws = _ws(0, q, ws)
@@ -328,7 +355,9 @@ def pa_paged_attend(q, cu_q, kv_len, block_table, k_pages, v_pages, max_q: int, 
     stride = _table(block_table, B)
     _pages(k_pages, v_pages, q.dtype, None, d)
     n_pages, page_size, hkv, _ = k_pages.shape
-    o, lse = _attend_outputs(q, o, lse, want_lse)
+    o, lse = _attend_outputs(q, o, lse, want_lse,
+                             [("q", q), ("cu_q", cu_q), ("kv_len", kv_len), ("block_table", block_table),
+                              ("k_pages", k_pages), ("v_pages", v_pages)])
     if ws is None:
         ws = _ws(pa_paged_attend_workspace_size(B, N, int(max_q), block_table.shape[1], page_size, hq, hkv, d, dt),
                  q, None)

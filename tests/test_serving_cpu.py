@@ -154,6 +154,34 @@ def test_binding_refuses_mismatched_tensors(S, monkeypatch):
     bad("cu_q", sc, kv, kv, table, pos, 16, 4, cu_q=pos[:2])
 
 
+def test_binding_refuses_outputs_over_inputs(S, monkeypatch):
+    monkeypatch.setattr(S, "_on", lambda *ts: None)
+    i32, bf = torch.int32, torch.bfloat16
+    flat = torch.zeros(40 * 8 * 64, dtype=bf)
+    q, k, v = flat[:10 * 8 * 64].view(10, 8, 64), torch.zeros((10, 2, 64), dtype=bf), torch.zeros((10, 2, 64), dtype=bf)
+    late = flat[512:512 + 10 * 8 * 64]          # q, one token later
+    cu, kv, pos = torch.zeros(3, dtype=i32), torch.zeros(2, dtype=i32), torch.zeros(10, dtype=i32)
+    table, kp = torch.zeros((2, 4), dtype=i32), torch.zeros((6, 16, 2, 64), dtype=bf)
+    vp = torch.zeros_like(kp)
+    ints = torch.zeros(40, dtype=i32)
+
+    def bad(match, f, *a, **kw):
+        with pytest.raises(ValueError, match=match):
+            f(*a, **kw)
+    pr, pg, ap, sc = S.pa_prompt_attend, S.pa_paged_attend, S.pa_paged_append, S.pa_paged_schedule
+    bad("o: overlaps q", pr, q, k, v, cu, o=late)
+    bad("o: overlaps lse", pr, q, k, v, cu, o=flat[10240:15360], lse=flat[10240:].view(torch.float32))
+    bad("o: overlaps v_pages", pg, q, cu, kv, table, kp, vp, 1, o=vp.view(-1)[:5120])
+    bad("q_out: overlaps q", ap, q, k, v, pos, pos.clone(), kp, vp, q_out=late)
+    bad("q_out: overlaps k_pages", ap, q, k, v, pos, pos.clone(), kp, vp, q_out=kp.view(-1)[64:])
+    bad("k_out: overlaps v_new", ap, q, k, v, pos, pos.clone(), kp, vp, k_out=v)
+    bad("k_pages: overlaps v_pages", ap, q, k, v, pos, pos.clone(), kp, kp)
+    bad("v_pages: overlaps k_new", ap, q, vp.view(-1, 2, 64)[3:13], v, pos, pos.clone(), kp, vp)
+    bad("kv_len_out: overlaps kv_len", sc, ints[20:22], ints[:2], table, pos, 16, 4, kv_len_out=ints[1:3])
+    bad("positions: overlaps slots", sc, kv, kv, table, pos, 16, 4, positions=ints[:4], slots=ints[3:8])
+    bad("block_table: overlaps free_pages", sc, kv, kv, table, table.view(-1), 16, 4)
+
+
 def test_oracle_attention_against_library_attention():
     g = torch.Generator().manual_seed(1)
     q, k, v = (torch.randn((n, h, 32), generator=g, dtype=torch.float64) for n, h in ((7, 6), (19, 2), (19, 2)))
