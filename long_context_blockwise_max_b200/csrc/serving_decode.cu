@@ -33,6 +33,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kKT = 32;      // keys per warp tile
 constexpr int kStages = 3;
+constexpr int kMergeAhead = 8;   // parts of a cut pair that are loaded together
 static_assert(kWarps * kKT == kPlanTile, "a block's step is one planned key group");
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -236,15 +237,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
         // and a non-finite value is taken out of the product and noted (the
         // rows that see it get it at the end)
         uint8_t* v = ring + st * C::STAGE + C::TILE;
-        for (int i = lane; i < kKT * C::CH; i += 32) {
+        const int n_keys = cur.kv - key0;
+#pragma unroll
+        for (int i = 0; i < C::CH; ++i) {
+          const int x = i * 32 + lane;
+          if (x / C::CH >= n_keys) *reinterpret_cast<uint4*>(v + swz<D>(x / C::CH, x % C::CH)) = make_uint4(0, 0, 0, 0);
+        }
+        // (a single new token sees every key there is)
+        const int hidden = max(0, ctx + 1 - key0), end = min(n_keys, kKT);
+        for (int i = hidden * C::CH + lane; i < end * C::CH; i += 32) {
           const int key = key0 + i / C::CH, c = i % C::CH;
-          if (key <= ctx) continue;
-          uint4* chunk = reinterpret_cast<uint4*>(v + swz<D>(i / C::CH, c));
-          if (key >= cur.kv) {
-            *chunk = make_uint4(0, 0, 0, 0);
-            continue;
-          }
-          uint16_t* e = reinterpret_cast<uint16_t*>(chunk);
+          uint16_t* e = reinterpret_cast<uint16_t*>(v + swz<D>(i / C::CH, c));
           for (int k = 0; k < 8; ++k)
             if ((e[k] & 0x7f80) == 0x7f80) {
               atomicMin(&bad[((e[k] & 0x7f) ? 2 : (e[k] >> 15)) * D + 8 * c + k], key);
@@ -424,17 +427,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
       }
       __syncthreads();
       if (flag[1]) {
-        // the last to arrive: all parts, in order, four at a time (their
-        // loads go out together; an online softmax over the groups of four)
+        // the last to arrive: all parts, in order, eight at a time (their
+        // loads go out together; an online softmax over the groups of eight)
         const int parts = c_hi - c_lo + 1;
         for (int i = threadIdx.x; i < rows * C::CH; i += kWarps * 32) {
           const int r = i / C::CH, c = i % C::CH;
           float M = -INFINITY, L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          for (int p0 = 0; p0 < parts; p0 += 4) {
-            float ls[4];
-            float4 x[4], y[4];
+          for (int p0 = 0; p0 < parts; p0 += kMergeAhead) {
+            float ls[kMergeAhead];
+            float4 x[kMergeAhead], y[kMergeAhead];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
+            for (int p = 0; p < kMergeAhead; ++p) {
               ls[p] = -INFINITY;
               if (p0 + p < parts) {
                 const int64_t at = static_cast<int64_t>(slot_of(c_lo + p0 + p)) * 16 + r;
@@ -444,7 +447,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
                 y[p] = __ldcg(src + 1);
               }
             }
-            const float m = fmaxf(fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3])), M);
+            float m = M;
+#pragma unroll
+            for (int p = 0; p < kMergeAhead; ++p) m = fmaxf(m, ls[p]);
             const float sub = m == -INFINITY ? 0.f : m;
             const float old = expf(M - sub);
             M = m;
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] *= old;
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
+            for (int p = 0; p < kMergeAhead; ++p) {
               const float f = expf(ls[p] - sub);
               L += f;
               if (p0 + p < parts && f != 0.f) {   // (zero: a part without a visible key)

@@ -127,16 +127,30 @@ template <int D>
 __device__ void guard_tile(uint8_t* v, int first_row, int n_keys, int key0, int piece, SvBars* bars, int tid) {
   using C = SvCfg<D>;
   constexpr int CH = D / 8;   // 16-byte chunks of a row
-  for (int i = first_row * CH + tid; i < 128 * CH; i += 64) {
-    const int r = i / CH, c = i % CH;
-    uint4* p = reinterpret_cast<uint4*>(v + (c >> 3) * C::KB_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-    if (r >= n_keys) {
-      *p = make_uint4(0, 0, 0, 0);
-      continue;
+  constexpr int STEP = 64 / CH;   // rows that the threads take together
+  const int c = tid % CH;
+  auto at = [&](int r) {
+    return reinterpret_cast<uint4*>(v + (c >> 3) * C::KB_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+  };
+#pragma unroll 4
+  for (int r = max(n_keys, 0) + tid / CH; r < 128; r += STEP) *at(r) = make_uint4(0, 0, 0, 0);
+  const int end = min(n_keys, 128);
+  // (eight loads at a time: one by one, their latency made a full tile take longer than its softmax)
+  for (int r0 = first_row + tid / CH; r0 < end; r0 += 8 * STEP) {
+    uint4 x[8];
+    uint32_t odd = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = make_uint4(0, 0, 0, 0);
+      if (r0 + j * STEP < end) x[j] = *at(r0 + j * STEP);
     }
-    uint4 x = *p;
-    if (bf16_nonfinite(x.x) || bf16_nonfinite(x.y) || bf16_nonfinite(x.z) || bf16_nonfinite(x.w)) {
-      uint16_t* e = reinterpret_cast<uint16_t*>(&x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      odd |= (bf16_nonfinite(x[j].x) || bf16_nonfinite(x[j].y) || bf16_nonfinite(x[j].z) || bf16_nonfinite(x[j].w))
+             << j;
+    for (; odd != 0; odd &= odd - 1) {
+      const int r = r0 + (__ffs(odd) - 1) * STEP;
+      uint16_t* e = reinterpret_cast<uint16_t*>(at(r));
       for (int k = 0; k < 8; ++k)
         if ((e[k] & 0x7f80) == 0x7f80) {
           const int kind = (e[k] & 0x7f) ? 2 : (e[k] >> 15);
@@ -145,7 +159,6 @@ __device__ void guard_tile(uint8_t* v, int first_row, int n_keys, int key0, int 
                         static_cast<uint32_t>(key0 + r));
           e[k] = 0;
         }
-      *p = x;
       bars->odd[piece & 1] = piece + 1;
     }
   }
