@@ -7,9 +7,12 @@
 // threads as 16 x 16: a thread has ROWS / 16 rows x 4 keys of the scores and
 // the same rows x D / 16 columns of o.  Online softmax in log2 units, the
 // running maximum and sum of a row kept by the 16 threads that share it.
-// With 64 rows the fp32 FMAs and the shared-memory reads that feed them (12
-// to 16 per 64 FMAs) are about even; with 16 rows (few new tokens) the reads
-// bound it.
+// With 64 rows the fp32 FMAs and the shared-memory wavefronts that feed them
+// (about 0.9 of a cycle per FMA cycle) are nearly even, and neither is hidden
+// in full: one 2048-token prompt, 4 / 2 heads of 64, takes 84 us of the call's
+// 89 (FMA pipe 52 %, LSU 64 % busy), one of 8192 tokens, 8 / 2 heads, 1.80 ms =
+// 38 TFLOP/s.  Threads with 8 rows read less, but only half as many fit the
+// registers: the same time.  With 16 rows (few new tokens) the reads bound it.
 #include "serving.h"
 
 namespace pa {
@@ -190,7 +193,20 @@ __global__ void __launch_bounds__(256, 2) attend_simt_kernel(AttendArgs a) {
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < 2 * CV; ++j) part[i][j] = make_float2(0.f, 0.f);
-    if (whole) {
+    bool plain = whole;
+    if (!whole) {
+      // Some row does not see some key: there a masked key must add nothing
+      // even if its V is not finite.  With finite V its zero probability does.
+      bool odd = false;
+#pragma unroll 4
+      for (int e = tid; e < kKeys * (D / 4); e += 256) {
+        const float4 x = reinterpret_cast<const float4*>(sv)[e];
+        odd |= !(fabsf(x.x) < INFINITY) || !(fabsf(x.y) < INFINITY) || !(fabsf(x.z) < INFINITY) ||
+               !(fabsf(x.w) < INFINITY);
+      }
+      plain = !__syncthreads_or(odd);
+    }
+    if (plain) {
 #pragma unroll 2
       for (int key = 0; key < kKeys; key += 4) {
         float p[R][4];
@@ -211,8 +227,7 @@ __global__ void __launch_bounds__(256, 2) attend_simt_kernel(AttendArgs a) {
           }
       }
     } else {
-      // some row does not see some key: there a masked key must add nothing
-      // even if its V is not finite, so its product is skipped
+      // its product is skipped
 #pragma unroll 1
       for (int key = 0; key < kKeys; ++key) {
 #pragma unroll
