@@ -421,6 +421,13 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       }
       // 32 columns at a time; with one row tile each warpgroup writes half of them
       const int c_lo = two ? 0 : t * (D / 2), c_hi = two ? D : c_lo + D / 2;
+      // (below, four lanes write 64 bytes of a row: rows 8 x + lane / 4 of the warp)
+      int at[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int row = sub * 32 + 8 * x + (lane >> 2), tk = static_cast<int>((row * ginv) >> 16);
+        at[x] = row < rows ? (tk * a.hq + (row - tk * g)) * D + 8 * (lane & 3) : -1;
+      }
 #pragma unroll 1
       for (int c = c_lo; c < c_hi; c += 32) {
         uint32_t ov[32];
@@ -452,14 +459,14 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
                 make_uint4(pack2(v[8 * e], v[8 * e + 1]), pack2(v[8 * e + 2], v[8 * e + 3]),
                            pack2(v[8 * e + 4], v[8 * e + 5]), pack2(v[8 * e + 6], v[8 * e + 7]));
           __syncwarp();
+          uint4 w[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int r = 8 * x + (lane >> 2), ch = lane & 3, row = sub * 32 + r;
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
-            const int tk = static_cast<int>((row * ginv) >> 16);
-            if (row < rows)
-              *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(tk) * a.hq + (row - tk * g)) * D + c + 8 * ch) = w;
-          }
+          for (int x = 0; x < 4; ++x)
+            w[x] = *reinterpret_cast<const uint4*>(stage + (8 * x + (lane >> 2)) * 64 +
+                                                   (((lane & 3) ^ ((lane >> 3) & 3)) << 4));
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (at[x] >= 0) *reinterpret_cast<uint4*>(out + at[x] + c) = w[x];
         }
       }
       if (odd) {
