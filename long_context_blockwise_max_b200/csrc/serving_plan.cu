@@ -18,7 +18,11 @@ namespace {
 
 constexpr int kBuckets = 256;
 // Cutting keys is looked at while the rows give less than three waves of
-// blocks: from there on there is nothing to gain.
+// blocks (prompts: from there on no row group is deeper than a block's share of
+// the work) or less than 16 (paged rows: one long cache among short ones would
+// be alone at the end.  512 tokens over 128K keys beside 64 x 128 over 1K: 1960 us
+// whole, 1076 us cut; looking in vain costs 3 us).
+constexpr int kPromptWaves = 3, kPagedWaves = 16;
 constexpr int kCuts = 32;
 constexpr int kMaxCut = 64;
 constexpr int kMaxCutItems = 1024;
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     const int n = static_cast<int>(item_base < most ? item_base : most);
     if (item_base > most && tid == 0) set_status(a.status, PA_ERR_INVALID, a.B);
     const int64_t blocks = static_cast<int64_t>(n) * a.hkv;
-    bool cut = a.part_cap > 0 && n > 0 && blocks < 3 * a.slots && n <= kMaxCutItems && deepest > 1;
+    bool cut = a.part_cap > 0 && n > 0 && n <= kMaxCutItems && deepest > 1;
     int parts = 1;
     if (cut) {
       for (int i = tid; i < n; i += threads) {
@@ -167,7 +171,8 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
       __syncthreads();
       // the number of cuts of the deepest rows that ends first: blocks run in
       // waves of one per slot, or, past one wave, fill the slots evenly with
-      // half a piece of slack; a cut adds the merge of its partial results.
+      // half a piece of slack (less with many waves: the shortest are last); a
+      // cut adds the merge of its partial results.
       // One lane per number, the rows spread over the warps.
       const int cuts = lane < 20 ? lane + 1 : min(kMaxCut, 20 + (lane - 19) * 4);   // 1 .. 20, then every fourth
       const int c = (deepest + cuts - 1) / cuts;
@@ -191,7 +196,8 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
         const float piece = a.piece_cost + c;   // the longest piece
         float cost = piece;
         if (static_cast<int64_t>(cost_pieces[lane]) * a.hkv > a.slots)
-          cost = fmaxf(cost, (cost_load[lane] + a.piece_cost * cost_pieces[lane]) * a.hkv / a.slots + 0.5f * piece);
+          cost = fmaxf(cost, (cost_load[lane] + a.piece_cost * cost_pieces[lane]) * a.hkv / a.slots +
+                                 0.5f * piece * fminf(1.f, 3.f * a.slots / blocks));
         if (cuts > 1) cost += a.merge_cost * (1.f + cuts / 24.f);
         if (cost_cuts[lane] > a.part_cap || cuts > deepest) cost = INFINITY;
         const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));
@@ -428,7 +434,7 @@ size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws) {
   a.part_cap = 0;
   a.item_cap = 0;
   const int64_t cuts = 2 * a.slots / a.hkv;   // partial results per kv head: two waves of blocks
-  if (a.tiles && full * a.hkv < 3 * a.slots && cuts >= 2 && deep > 1) {
+  if (a.tiles && full * a.hkv < (a.max_q > 0 ? kPagedWaves : kPromptWaves) * a.slots && cuts >= 2 && deep > 1) {
     const int64_t most = groups * deep;
     a.part_cap = static_cast<int>(most < cuts ? most : cuts);
     a.item_cap = static_cast<int>(groups < a.part_cap ? groups : a.part_cap);   // rows that are cut
