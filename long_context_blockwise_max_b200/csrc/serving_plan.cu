@@ -26,6 +26,9 @@ constexpr int kPromptWaves = 3, kPagedWaves = 16;
 constexpr int kCuts = 32;
 constexpr int kMaxCut = 64;
 constexpr int kMaxCutItems = 1024;
+// key tiles of 2.1 us per block.  32 requests, four of them tokens behind up to
+// 27 keys: 108 us with the decode kernel at work, 97 us without.
+constexpr int kFewTiles = 3;
 // K and V of this many bytes stay in L2 (126 MB) beside q and o.  Pieces of
 // more, but of no more than two waves per head, are also taken over all heads
 // in order of depth: a balanced end is worth more than the reuse.
@@ -34,7 +37,6 @@ constexpr double kL2Keys = 100e6;
 struct Lens {
   int64_t row0, q, kv;
   int rows;      // packed (token, head) rows per kv head
-  bool small;    // decode kernel
 };
 
 __device__ __forceinline__ Lens lens_of(const AttendArgs& a, int b, int64_t max_kv, bool record) {
@@ -51,7 +53,6 @@ __device__ __forceinline__ Lens lens_of(const AttendArgs& a, int b, int64_t max_
   }
   const int64_t rows = r.q * (a.hq / a.hkv);
   r.rows = static_cast<int>(rows < INT32_MAX ? rows : INT32_MAX);
-  r.small = r.rows <= a.small_rows;
   return r;
 }
 
@@ -79,6 +80,7 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
   __shared__ int hist[kBuckets];
   __shared__ int depth[kMaxCutItems], part_of[kMaxCutItems], first_piece[kMaxCutItems + 1];
   __shared__ int deepest, n_merge;
+  __shared__ int few[3];   // deepest chunk, deepest request of few rows, key tiles of those
   __shared__ unsigned key_tiles;
   __shared__ int cost_pieces[kCuts], cost_cuts[kCuts], cost_load[kCuts], best;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
@@ -93,7 +95,37 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     key_tiles = 0;
   }
   if (tid < kCuts) cost_pieces[tid] = cost_cuts[tid] = cost_load[tid] = 0;
+  if (tid < 3) few[tid] = 0;
   __syncthreads();
+  // Few generated tokens with short caches beside chunks: the decode kernel
+  // takes 8 us whatever it has to do, and 2 us for nothing.  They are the tile
+  // kernel's when its blocks need less for them (kFewTiles key tiles each) and
+  // no cache is longer than the chunks' longest.
+  int small_rows = a.small_rows;
+  if (a.tiles && small_rows > 0) {
+    int cost = 0, deep_small = 0, deep = 0;
+    for (int b = tid; b < a.B; b += threads) {
+      const Lens r = lens_of(a, b, max_kv, false);
+      if (r.q <= 0) continue;
+      const int d = static_cast<int>((r.kv + kPlanTile - 1) / kPlanTile);
+      if (r.rows > small_rows) {
+        deep = max(deep, d);
+      } else {
+        deep_small = max(deep_small, d);
+        cost = min(cost + d + static_cast<int>(a.piece_cost), 1 << 20);
+      }
+    }
+    deep = __reduce_max_sync(0xffffffffu, deep);
+    deep_small = __reduce_max_sync(0xffffffffu, deep_small);
+    cost = __reduce_add_sync(0xffffffffu, cost);
+    if (lane == 0) {
+      atomicMax(&few[0], deep);
+      atomicMax(&few[1], deep_small);
+      atomicAdd(&few[2], min(cost, 1 << 20));
+    }
+    __syncthreads();
+    if (few[1] <= few[0] && static_cast<int64_t>(few[2]) * a.hkv <= kFewTiles * a.slots) small_rows = 0;
+  }
   int64_t item_base = 0, unit_base = 0;
   for (int b0 = 0; b0 < a.B; b0 += threads) {
     const int b = b0 + tid;
@@ -102,7 +134,7 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     if (b < a.B) {
       const Lens r = lens_of(a, b, max_kv, true);
       if (r.q > 0) {
-        if (r.small) {
+        if (r.rows <= small_rows) {
           const int64_t groups = (r.kv + kPlanTile - 1) / kPlanTile;
           nu = (groups > 0 ? groups : 1) * a.hkv;
         } else {
