@@ -27,6 +27,15 @@
 // softmax warps store a piece's output: one block per piece took 8 us of
 // set-up and output per piece beside 2.1 us per key tile.
 //
+// What bounds it: the chain of a row tile's softmax (2300 clocks: TMEM load 120,
+// maximum 410, exponentials 1290, sums and P 500) and its PV and next QK^T
+// (1230), 3600 to 3900 clocks per pair of row tiles and key tile, in which the
+// tensor pipe and the exponentials are each 54 % busy; TMEM has no room for a
+// second S.  A piece's output takes another 3800 (64 KB out of one SM).  32 / 8
+// heads of 128: one 32K prompt 8.0 to 8.2 ms = 1070 to 1100 TFLOP/s at the power
+// cap (7.0 ms before it sets in); 24 prompts of 1 to 4096 tokens 160 us; a 64-token
+// query over 128K keys 170 to 180 us with its plan and merge.
+//
 // Guard: P is zero at a masked key, but zero times an infinity or NaN in its
 // V is NaN.  In tiles with keys that some row does not see, rows past the
 // request's last key are zeroed in shared memory, and a non-finite V element
