@@ -395,6 +395,41 @@ def test_paged_the_most_requests(S, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("q_lens,kv_lens", [
+    ([17] * 14 + [33] + [17] * 15, [40 + i for i in range(14)] + [3000] + [17 + 9 * i for i in range(15)]),
+    ([20, 260, 1] * 11, [2500, 260, 1] + [30, 270, 60] * 10),
+])
+def test_paged_a_long_cache_beside_many_short_ones(S, dtype, q_lens, kv_lens):
+    # more than three waves of row groups, and still the long one's keys are cut
+    c = paged_batch(q_lens, kv_lens, 16, 16, 64, 16, DTYPES[dtype], seed=31)
+    o, lse, ws = S.pa_paged_attend(c["q"], c["cu_q"], c["kv_len"], c["table"], c["k_pages"], c["v_pages"], c["max_q"])
+    assert ok(S, ws) == 0
+    check_paged(c, o, lse, "long beside short")
+
+
+@pytest.mark.parametrize("bad", [0.0, float("inf"), float("nan")])
+@pytest.mark.parametrize("q_lens,kv_lens", [
+    ([70, 1, 2, 1], [900, 30, 2, 300]),          # the few tokens' keys are few: one kernel for all
+    ([70, 1, 2, 1], [900, 30, 2, 1400]),         # a cache longer than the chunk's: the decode kernel
+    ([2, 1, 40, 0, 1], [1, 0, 40, 9, 128]),      # rows and requests without a key
+])
+def test_paged_few_tokens_beside_a_chunk(S, q_lens, kv_lens, bad):
+    c = paged_batch(q_lens, kv_lens, 8, 2, 128, 16, torch.bfloat16, seed=32)
+    args = (c["cu_q"], c["kv_len"], c["table"])
+    o, lse, ws = S.pa_paged_attend(c["q"], *args, c["k_pages"], c["v_pages"], c["max_q"])
+    assert ok(S, ws) == 0
+    check_paged(c, o, lse, "few tokens")
+    # what the pages hold behind the last key changes nothing
+    k, v = c["k_pages"].clone(), c["v_pages"].clone()
+    for b, n in enumerate(kv_lens):
+        for key in range(n, -(-n // 16) * 16):
+            page = int(c["table"][b, key // 16])
+            k[page, key % 16], v[page, key % 16] = bad, bad
+    o1, lse1, ws = S.pa_paged_attend(c["q"], *args, k, v, c["max_q"])
+    assert ok(S, ws) == 0 and torch.equal(o, o1) and torch.equal(lse, lse1)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [300, 200]), ([4], [300]), ([70], [400]), ([200], [200])])
 def test_a_bad_query_row_touches_no_other(S, dtype, bad, q_lens, kv_lens):
