@@ -149,7 +149,13 @@ PyObject* paged_schedule(PyObject*, PyObject* const* args, Py_ssize_t n) {
         static_cast<int32_t>(page), tokens, p, p + B + 1, p + 2 * B + 1, p + 2 * B + 1 + tokens,
         p + 2 * B + 1 + 2 * tokens, ws.data_ptr(), 256, a.stream());
     if (rc != PA_OK) return PyLong_FromLong(rc);
-    auto part = [&](int64_t from, int64_t count) { return all.as_strided({count}, {1}, from); };
+    // (tensors over its storage, put together here: five dispatched views took as long as the launch)
+    auto part = [&](int64_t from, int64_t count) {
+      Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+      t.unsafeGetTensorImpl()->set_storage_offset(from);
+      t.unsafeGetTensorImpl()->set_sizes_contiguous({count});
+      return t;
+    };
     return result(rc, part(0, B + 1), part(B + 1, B), part(2 * B + 1, tokens), part(2 * B + 1 + tokens, tokens),
                   part(2 * B + 1 + 2 * tokens, 1), ws);
   });
