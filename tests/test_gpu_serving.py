@@ -1,6 +1,11 @@
 """Serving operators on the GPU against the fp64 / integer oracle: page
 tables and slot maps, rotate-and-append, packed prompt attention, paged
 attention, and a whole step of them in the order of use."""
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -523,6 +528,52 @@ def test_calls_on_two_streams_and_repeated(S):
         torch.cuda.synchronize()
         for o, lse in ((o1, lse1), (o2, lse2)):
             assert torch.equal(o, o0) and torch.equal(lse, lse0)
+
+
+def test_calls_from_several_threads(S):
+    c = paged_batch([1, 64, 5], [30, 200, 90], 8, 2, 64, 16, torch.bfloat16, seed=33)
+    args = (c["q"], c["cu_q"], c["kv_len"], c["table"], c["k_pages"], c["v_pages"], c["max_q"])
+    want, want_lse, _ = S.pa_paged_attend(*args)
+    torch.cuda.synchronize()
+    wrong, done = [], []
+
+    def work(i):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            got = [S.pa_paged_attend(*args)[:2] for _ in range(20)]
+            side.synchronize()
+        wrong.extend(i for o, lse in got if not (torch.equal(o, want) and torch.equal(lse, want_lse)))
+        done.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and len(done) == 4
+
+
+FIRST_CALL = """
+import torch
+from long_context_blockwise_max_b200 import serving as S
+q = torch.randn(70, 8, 64, device="cuda").bfloat16()
+k, v = (torch.randn(40, 16, 2, 64, device="cuda").bfloat16() for _ in range(2))
+cu, kv = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 1, 65, 70], [30, 200, 90]))
+t = torch.arange(39, dtype=torch.int32, device="cuda").view(3, 13)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    o, lse, ws = S.pa_paged_attend(q, cu, kv, t, k, v, 64)
+g.replay()
+o1, lse1, _ = S.pa_paged_attend(q, cu, kv, t, k, v, 64)
+assert torch.equal(o, o1) and torch.equal(lse, lse1)
+print("captured")
+"""
+
+
+def test_a_process_may_capture_its_first_call():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and "captured" in got.stdout, got.stderr[-2000:]
 
 
 def test_captured_step_follows_its_inputs(S):
