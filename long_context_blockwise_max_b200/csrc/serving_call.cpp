@@ -16,6 +16,9 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <initializer_list>
+#include <utility>
+
 #include "../../include/pulsar_serving.h"
 
 namespace {
@@ -92,6 +95,26 @@ struct Args {
   void* stream() const { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
 };
 
+// Whether a tensor's elements share an address with another's: what a kernel
+// writes must not be read or written by another of its blocks.  (The spans of
+// serving.py, which refuses such a call with a message.)
+bool overlap(const Tensor& a, std::initializer_list<const Tensor*> others) {
+  auto span = [](const Tensor& t) {
+    int64_t last = 0;
+    for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
+    const char* first = static_cast<const char*>(t.const_data_ptr());
+    return std::make_pair(first, first + (last + 1) * static_cast<int64_t>(t.element_size()));
+  };
+  if (a.numel() == 0) return false;
+  const auto x = span(a);
+  for (const Tensor* t : others) {
+    if (t->numel() == 0) continue;
+    const auto y = span(*t);
+    if (x.first < y.second && y.first < x.second) return true;
+  }
+  return false;
+}
+
 int dtype_of(const Tensor& t) {
   return t.scalar_type() == at::kBFloat16 ? PA_BF16 : t.scalar_type() == at::kFloat ? PA_F32 : -1;
 }
@@ -138,7 +161,8 @@ PyObject* paged_schedule(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const Tensor* table = a.table(2, q ? q->numel() : 0, &stride);
     const Tensor* pool = a.ints(3, 0);
     const int64_t page = a.integer(4), tokens = a.integer(5);
-    if (!a.ok || tokens < 0 || pool->numel() > kMaxInt || q->numel() > 8192) return to_slow();
+    if (!a.ok || tokens < 0 || pool->numel() > kMaxInt || q->numel() > 8192 || overlap(*table, {q, kv, pool}))
+      return to_slow();
     const int64_t B = q->numel();
     // one allocation, in the order of the results
     Tensor all = a.make({2 * B + 2 * tokens + 2}, at::kInt), ws = a.make({256}, at::kByte);
@@ -187,7 +211,8 @@ PyObject* paged_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int type = dtype_of(*k);
     if (!a.ok || type < 0 || q->scalar_type() != k->scalar_type() || v->scalar_type() != k->scalar_type() ||
         v->sizes() != k->sizes() || q->size(0) != N || q->size(2) != d || N > kMaxInt || hq > kMaxInt ||
-        !cache_ok(kp, vp, k->scalar_type(), d) || kp->size(2) != hkv || kp->data_ptr() == vp->data_ptr())
+        !cache_ok(kp, vp, k->scalar_type(), d) || kp->size(2) != hkv || overlap(*kp, {vp, q, k, v, pos, slots}) ||
+        overlap(*vp, {q, k, v, pos, slots}))
       return to_slow();
     Tensor q_out = a.make({N, hq, d}, q->scalar_type()), k_out, ws = a.make({256}, at::kByte);
     if (PyObject_IsTrue(args[8])) k_out = a.make({N, hkv, d}, k->scalar_type());

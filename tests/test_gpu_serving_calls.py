@@ -1,0 +1,64 @@
+"""The serving operators' calls from Python on CUDA tensors: what the ordinary
+call refuses."""
+import pytest
+import torch
+
+from serving_cases import randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def S():
+    from long_context_blockwise_max_b200 import serving
+    assert torch.cuda.is_available()
+    return serving
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def test_the_ordinary_append_refuses_pages_over_its_inputs(S):
+    bf = torch.bfloat16
+    both = torch.zeros(2 * 6 * 16 * 2 * 64 + 64, dtype=bf, device="cuda")
+    size = 6 * 16 * 2 * 64
+    kp, vp = both[:size].view(6, 16, 2, 64), both[size:2 * size].view(6, 16, 2, 64)
+    q, k, v = randn((10, 8, 64), bf, 1), randn((10, 2, 64), bf, 2), randn((10, 2, 64), bf, 3)
+    pos, slots = i32(range(10)), i32(range(20, 30))
+
+    def bad(match, *args):
+        with pytest.raises(ValueError, match=match):
+            S.pa_paged_append(*args, rope_theta=1e4)
+    bad("k_pages: overlaps v_pages", q, k, v, pos, slots, kp, kp)
+    bad("k_pages: overlaps v_pages", q, k, v, pos, slots, kp, both[size - 64:2 * size - 64].view(6, 16, 2, 64))
+    for pages, name in ((kp, "k_pages"), (vp, "v_pages")):
+        rows = pages.view(-1, 2, 64)
+        bad(f"{name}: overlaps k_new", q, rows[86:96], v, pos, slots, kp, vp)
+        bad(f"{name}: overlaps v_new", q, k, rows[:10], pos, slots, kp, vp)
+        bad(f"{name}: overlaps q", pages.view(-1, 8, 64)[14:24], k, v, pos, slots, kp, vp)
+        bad(f"{name}: overlaps positions", q, k, v, rows.view(torch.int32).view(-1)[-10:], slots, kp, vp)
+        bad(f"{name}: overlaps slots", q, k, v, pos, rows.view(torch.int32).view(-1)[:10], kp, vp)
+    # neighbours do not overlap
+    assert both.eq(0).all()
+    qr, _, ws = S.pa_paged_append(q, k, v, pos, slots, kp, vp, rope_theta=1e4)
+    assert S.pulsar.pa_workspace_status(ws) == 0
+    assert torch.equal(vp.view(-1, 2, 64)[20:30], v) and both[2 * size:].eq(0).all() and both[:20 * 128].eq(0).all()
+
+
+def test_the_ordinary_schedule_refuses_a_table_over_its_inputs(S):
+    ints = torch.arange(40, dtype=torch.int32, device="cuda")
+    before = ints.clone()
+    table, other = ints[8:24].view(2, 8), i32([3, 4])
+
+    def bad(match, *args):
+        with pytest.raises(ValueError, match=match):
+            S.pa_paged_schedule(*args, 16, 4)
+    bad("block_table: overlaps q_len", ints[7:9], other, table, ints[30:])
+    bad("block_table: overlaps kv_len", other, ints[23:25], table, ints[30:])
+    bad("block_table: overlaps free_pages", other, other, table, ints[20:])
+    bad("block_table: overlaps free_pages", other, other, ints[8:24].view(2, 8)[:, :4], ints[15:20])
+    torch.cuda.synchronize()
+    assert torch.equal(ints, before)
+    cu, kv, pos, slots, used, ws = S.pa_paged_schedule(other, ints[:2], table, ints[24:], 16, 7)
+    assert S.pulsar.pa_workspace_status(ws) == 0 and cu.tolist() == [0, 3, 7] and used.tolist() == [1]
