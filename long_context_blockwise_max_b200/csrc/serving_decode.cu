@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
             for (int p = 0; p < kMergeAhead; ++p) {
               const float f = expf(ls[p] - sub);
               L += f;
-              if (p0 + p < parts && f != 0.f) {   // (zero: a part without a visible key)
+              if (p0 + p < parts) {   // (a weight of zero too: a non-finite V that the row sees is not lost)
                 acc[0] += f * x[p].x; acc[1] += f * x[p].y; acc[2] += f * x[p].z; acc[3] += f * x[p].w;
                 acc[4] += f * y[p].x; acc[5] += f * y[p].y; acc[6] += f * y[p].z; acc[7] += f * y[p].w;
               }

@@ -403,8 +403,10 @@ __global__ void __launch_bounds__(256, 4) attend_merge_kernel(AttendArgs a) {
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) {
+        // (a weight of zero is multiplied too: a non-finite V that the row sees
+        // leaves its column non-finite however little its key weighs)
         const float wk = __shfl_sync(0xffffffffu, w, (p + k) & 31);
-        if (p + k < it.n_parts && wk != 0.f) {   // (zero: a piece without a visible key)
+        if (p + k < it.n_parts) {
 #pragma unroll
           for (int i = 0; i < VPL; ++i) acc[i] += wk * v[k][i];
         }
