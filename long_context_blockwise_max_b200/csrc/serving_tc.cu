@@ -83,7 +83,8 @@ struct SvBars {
   uint64_t v_ready[2];    // ... and has been checked
   uint64_t s_full[2], p_full[2], o_final[2];
   uint64_t noted[2];      // the guard is through with a piece's tiles; pieces in turn
-  uint64_t done[2];       // the softmax warps have read a piece's O and notes; pieces in turn
+  uint64_t done[2];       // the softmax warps have read a piece's O; pieces in turn
+  uint64_t read[2];       // they and the issuer have read its item, maxima and notes; pieces in turn
   uint64_t ml_full[2][2]; // a warpgroup's maxima and sums are written (one row tile); pieces in turn
   uint64_t work_full[2];  // `work` holds a piece; pieces in turn
   uint64_t drain;
@@ -121,7 +122,7 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 // An arrival that orders no memory (the caller's global stores need not be
-// done first); what it hands over is ordered by tcgen05 fences.
+// done first): for O in TMEM alone, whose reads tcgen05 fences order.
 __device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
   asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       mbar_init(&bars->o_final[s], 1);
       mbar_init(&bars->noted[s], 2);
       mbar_init(&bars->done[s], 8);
+      mbar_init(&bars->read[s], 9);
       mbar_init(&bars->ml_full[s][0], 4);
       mbar_init(&bars->ml_full[s][1], 4);
       mbar_init(&bars->work_full[s], 1);
@@ -428,6 +430,14 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
         if (it.part >= 0) a.part_lse[prow] = lse;
         else if (a.lse) a.lse[(static_cast<int64_t>(it.row0) + tok_t + rt) * a.hq + it.kvh * g + rh] = lse;
       }
+      // What is read of shared memory is handed back by an ordinary arrival, which
+      // orders the reads before whoever writes there next: before the output,
+      // whose stores it would wait for, unless there are notes to read behind it.
+      auto hand_back = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->read[k & 1]);
+      };
+      if (!odd) hand_back();
       // 32 columns at a time; with one row tile each warpgroup writes half of them
       const int c_lo = two ? 0 : t * (D / 2), c_hi = two ? D : c_lo + D / 2;
       // (below, four lanes write 64 bytes of a row: rows 8 x + lane / 4 of the warp)
@@ -497,10 +507,11 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
             *x = __float2bfloat16_rn(__bfloat162float(*x) + add);
           }
         }
+        hand_back();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_relaxed(&bars->done[k & 1]);   // O and the notes have been read
+      if (lane == 0) mbar_arrive_relaxed(&bars->done[k & 1]);   // O has been read
     }
     if (!ok) fail(9);
   } else {
@@ -532,7 +543,10 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       Item it;
       for (int k = 0; ok; ++k) {
         // the slot's previous piece (two before) is finished
-        if (k >= 2 && !wait(&bars->done[k & 1], (k >> 1) - 1)) { ok = false; break; }
+        if (k >= 2 && !(wait(&bars->done[k & 1], (k >> 1) - 1) && wait(&bars->read[k & 1], (k >> 1) - 1))) {
+          ok = false;
+          break;
+        }
         if (lane == 0) {
           put_item(bars, k, tpt, after, kvh);
           mbar_arrive(&bars->work_full[k & 1]);
@@ -646,6 +660,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
         for (int k = 0; ok; ++k, tile += it.n) {
           if (!wait_one(&bars->work_full[k & 1], k >> 1)) { fail(2); break; }
           if (!get_item(bars, k, it)) break;
+          mbar_arrive(&bars->read[k & 1]);
           const int n = it.n;
           auto wait_v = [&](int jj) {
             const int st = (tile + jj) & 1;
