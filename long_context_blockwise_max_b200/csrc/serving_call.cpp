@@ -10,12 +10,14 @@
 //
 // Each returns a tuple of tensors (the last one is the workspace), a negative
 // pa_status as an int, or None.
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <exception>
 #include <initializer_list>
 #include <utility>
 
@@ -139,13 +141,14 @@ PyObject* result(int rc, T&&... tensors) {
   return out;
 }
 
-// C++ exceptions (an allocation that fails) become Python ones.
+// C++ exceptions become the Python ones that torch's own functions raise for
+// them (an allocation that fails: torch.OutOfMemoryError).
 template <typename F>
 PyObject* guarded(F&& f) {
   try {
     return f();
-  } catch (const std::exception& e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }

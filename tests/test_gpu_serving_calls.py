@@ -1,5 +1,5 @@
 """The serving operators' calls from Python on CUDA tensors: what the ordinary
-call refuses."""
+call refuses and raises."""
 import pytest
 import torch
 
@@ -62,3 +62,16 @@ def test_the_ordinary_schedule_refuses_a_table_over_its_inputs(S):
     assert torch.equal(ints, before)
     cu, kv, pos, slots, used, ws = S.pa_paged_schedule(other, ints[:2], table, ints[24:], 16, 7)
     assert S.pulsar.pa_workspace_status(ws) == 0 and cu.tolist() == [0, 3, 7] and used.tolist() == [1]
+
+
+def test_an_allocation_that_fails_raises_what_torch_raises(S):
+    lens, table = i32([3]), i32([[0, 0]])
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(0.02)      # below 4 GB; the call asks for 8 GB
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            S.pa_paged_schedule(lens, i32([0]), table, i32([0, 1]), 16, 2 ** 30)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    cu, kv, _, _, _, _ = S.pa_paged_schedule(lens, i32([0]), table, i32([0, 1]), 16, 3)
+    assert cu.tolist() == [0, 3] and kv.tolist() == [3]
