@@ -218,7 +218,9 @@ PyObject* paged_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
         overlap(*vp, {q, k, v, pos, slots}))
       return to_slow();
     Tensor q_out = a.make({N, hq, d}, q->scalar_type()), k_out, ws = a.make({256}, at::kByte);
-    if (PyObject_IsTrue(args[8])) k_out = a.make({N, hkv, d}, k->scalar_type());
+    const int want_k = PyObject_IsTrue(args[8]);
+    if (want_k < 0) return nullptr;   // (its error is set)
+    if (want_k) k_out = a.make({N, hkv, d}, k->scalar_type());
     const int rc = pa_paged_append(q->data_ptr(), k->data_ptr(), v->data_ptr(), type, N, ldq, ldk, ldv,
                                    static_cast<int32_t>(hq), static_cast<int32_t>(hkv), static_cast<int32_t>(d), theta,
                                    pos->data_ptr<int32_t>(), slots->data_ptr<int32_t>(), kp->data_ptr(),
@@ -248,7 +250,9 @@ PyObject* prompt_attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                                         static_cast<int32_t>(hkv), static_cast<int32_t>(d), type);
     if (need == 0) return to_slow();
     Tensor o = a.make({N, hq, d}, q->scalar_type()), lse, ws = a.make({static_cast<int64_t>(need)}, at::kByte);
-    if (PyObject_IsTrue(args[4])) lse = a.make({N, hq}, at::kFloat);
+    const int want_lse = PyObject_IsTrue(args[4]);
+    if (want_lse < 0) return nullptr;
+    if (want_lse) lse = a.make({N, hq}, at::kFloat);
     const int rc = pa_prompt_attend(q->data_ptr(), k->data_ptr(), v->data_ptr(), type, N, ldq, ldk, ldv,
                                     cu->data_ptr<int32_t>(), static_cast<int32_t>(B), static_cast<int32_t>(hq),
                                     static_cast<int32_t>(hkv), static_cast<int32_t>(d), o.data_ptr(),
@@ -283,7 +287,9 @@ PyObject* paged_attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                                        static_cast<int32_t>(d), type);
     if (need == 0) return to_slow();
     Tensor o = a.make({N, hq, d}, q->scalar_type()), lse, ws = a.make({static_cast<int64_t>(need)}, at::kByte);
-    if (PyObject_IsTrue(args[7])) lse = a.make({N, hq}, at::kFloat);
+    const int want_lse = PyObject_IsTrue(args[7]);
+    if (want_lse < 0) return nullptr;
+    if (want_lse) lse = a.make({N, hq}, at::kFloat);
     const int rc = pa_paged_attend(q->data_ptr(), type, N, ldq, cu->data_ptr<int32_t>(), kv->data_ptr<int32_t>(), b, mq,
                                    table->data_ptr<int32_t>(), stride, width, page, kp->data_ptr(), vp->data_ptr(),
                                    static_cast<int32_t>(kp->size(0)), static_cast<int32_t>(hq), hkv,

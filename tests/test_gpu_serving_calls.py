@@ -75,3 +75,20 @@ def test_an_allocation_that_fails_raises_what_torch_raises(S):
         torch.cuda.set_per_process_memory_fraction(1.0)
     cu, kv, _, _, _, _ = S.pa_paged_schedule(lens, i32([0]), table, i32([0, 1]), 16, 3)
     assert cu.tolist() == [0, 3] and kv.tolist() == [3]
+
+
+class Undecided:
+    def __bool__(self):
+        raise KeyError("neither")
+
+
+def test_a_choice_without_a_truth_value_raises_its_own_error(S):
+    q, k = randn((4, 4, 64), torch.bfloat16, 1), randn((4, 2, 64), torch.bfloat16, 2)
+    pages = torch.zeros((2, 1, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    row = i32(range(4))
+    for call in (lambda: S.pa_prompt_attend(q, k, k, i32([0, 4]), want_lse=Undecided()),
+                 lambda: S.pa_paged_attend(q, i32([0, 4]), i32([4]), i32([[0]]), pages[0], pages[1], 4,
+                                           want_lse=Undecided()),
+                 lambda: S.pa_paged_append(q, k, k, row, row, pages[0], pages[1], rope_theta=1e4, want_k=Undecided())):
+        with pytest.raises(KeyError, match="neither"):
+            call()
