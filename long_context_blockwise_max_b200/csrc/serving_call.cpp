@@ -153,6 +153,19 @@ PyObject* guarded(F&& f) {
   }
 }
 
+// The C entry point without the interpreter's lock: where the queue of launches
+// is full a launch waits for the GPU, and other threads go on meanwhile.  (The
+// caller holds its tensors.)
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename... P, typename... A>
+int launch(int (*entry)(P...), A... args) {
+  const Unlocked unlocked;
+  return entry(args...);
+}
+
 // (q_len, kv_len, block_table, free_pages, page_size, n_tokens)
 PyObject* paged_schedule(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -170,11 +183,11 @@ PyObject* paged_schedule(PyObject*, PyObject* const* args, Py_ssize_t n) {
     // one allocation, in the order of the results
     Tensor all = a.make({2 * B + 2 * tokens + 2}, at::kInt), ws = a.make({256}, at::kByte);
     int32_t* p = all.data_ptr<int32_t>();
-    const int rc = pa_paged_schedule(
-        q->data_ptr<int32_t>(), kv->data_ptr<int32_t>(), static_cast<int32_t>(B), table->data_ptr<int32_t>(), stride,
-        static_cast<int32_t>(table->size(1)), pool->data_ptr<int32_t>(), static_cast<int32_t>(pool->numel()),
-        static_cast<int32_t>(page), tokens, p, p + B + 1, p + 2 * B + 1, p + 2 * B + 1 + tokens,
-        p + 2 * B + 1 + 2 * tokens, ws.data_ptr(), 256, a.stream());
+    const int rc = launch(pa_paged_schedule, q->data_ptr<int32_t>(), kv->data_ptr<int32_t>(), static_cast<int32_t>(B),
+                          table->data_ptr<int32_t>(), stride, static_cast<int32_t>(table->size(1)),
+                          pool->data_ptr<int32_t>(), static_cast<int32_t>(pool->numel()), static_cast<int32_t>(page),
+                          tokens, p, p + B + 1, p + 2 * B + 1, p + 2 * B + 1 + tokens, p + 2 * B + 1 + 2 * tokens,
+                          ws.data_ptr(), 256, a.stream());
     if (rc != PA_OK) return PyLong_FromLong(rc);
     // (tensors over its storage, put together here: five dispatched views took as long as the launch)
     auto part = [&](int64_t from, int64_t count) {
@@ -221,11 +234,11 @@ PyObject* paged_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int want_k = PyObject_IsTrue(args[8]);
     if (want_k < 0) return nullptr;   // (its error is set)
     if (want_k) k_out = a.make({N, hkv, d}, k->scalar_type());
-    const int rc = pa_paged_append(q->data_ptr(), k->data_ptr(), v->data_ptr(), type, N, ldq, ldk, ldv,
-                                   static_cast<int32_t>(hq), static_cast<int32_t>(hkv), static_cast<int32_t>(d), theta,
-                                   pos->data_ptr<int32_t>(), slots->data_ptr<int32_t>(), kp->data_ptr(),
-                                   vp->data_ptr(), kp->size(0) * kp->size(1), q_out.data_ptr(),
-                                   k_out.defined() ? k_out.data_ptr() : nullptr, ws.data_ptr(), 256, a.stream());
+    const int rc = launch(pa_paged_append, q->data_ptr(), k->data_ptr(), v->data_ptr(), type, N, ldq, ldk, ldv,
+                          static_cast<int32_t>(hq), static_cast<int32_t>(hkv), static_cast<int32_t>(d), theta,
+                          pos->data_ptr<int32_t>(), slots->data_ptr<int32_t>(), kp->data_ptr(), vp->data_ptr(),
+                          kp->size(0) * kp->size(1), q_out.data_ptr(), k_out.defined() ? k_out.data_ptr() : nullptr,
+                          ws.data_ptr(), 256, a.stream());
     return result(rc, q_out, k_out, ws);
   });
 }
@@ -253,10 +266,10 @@ PyObject* prompt_attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int want_lse = PyObject_IsTrue(args[4]);
     if (want_lse < 0) return nullptr;
     if (want_lse) lse = a.make({N, hq}, at::kFloat);
-    const int rc = pa_prompt_attend(q->data_ptr(), k->data_ptr(), v->data_ptr(), type, N, ldq, ldk, ldv,
-                                    cu->data_ptr<int32_t>(), static_cast<int32_t>(B), static_cast<int32_t>(hq),
-                                    static_cast<int32_t>(hkv), static_cast<int32_t>(d), o.data_ptr(),
-                                    lse.defined() ? lse.data_ptr<float>() : nullptr, ws.data_ptr(), need, a.stream());
+    const int rc = launch(pa_prompt_attend, q->data_ptr(), k->data_ptr(), v->data_ptr(), type, N, ldq, ldk, ldv,
+                          cu->data_ptr<int32_t>(), static_cast<int32_t>(B), static_cast<int32_t>(hq),
+                          static_cast<int32_t>(hkv), static_cast<int32_t>(d), o.data_ptr(),
+                          lse.defined() ? lse.data_ptr<float>() : nullptr, ws.data_ptr(), need, a.stream());
     return result(rc, o, lse, ws);
   });
 }
@@ -290,11 +303,11 @@ PyObject* paged_attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int want_lse = PyObject_IsTrue(args[7]);
     if (want_lse < 0) return nullptr;
     if (want_lse) lse = a.make({N, hq}, at::kFloat);
-    const int rc = pa_paged_attend(q->data_ptr(), type, N, ldq, cu->data_ptr<int32_t>(), kv->data_ptr<int32_t>(), b, mq,
-                                   table->data_ptr<int32_t>(), stride, width, page, kp->data_ptr(), vp->data_ptr(),
-                                   static_cast<int32_t>(kp->size(0)), static_cast<int32_t>(hq), hkv,
-                                   static_cast<int32_t>(d), o.data_ptr(),
-                                   lse.defined() ? lse.data_ptr<float>() : nullptr, ws.data_ptr(), need, a.stream());
+    const int rc = launch(pa_paged_attend, q->data_ptr(), type, N, ldq, cu->data_ptr<int32_t>(),
+                          kv->data_ptr<int32_t>(), b, mq, table->data_ptr<int32_t>(), stride, width, page,
+                          kp->data_ptr(), vp->data_ptr(), static_cast<int32_t>(kp->size(0)), static_cast<int32_t>(hq),
+                          hkv, static_cast<int32_t>(d), o.data_ptr(), lse.defined() ? lse.data_ptr<float>() : nullptr,
+                          ws.data_ptr(), need, a.stream());
     return result(rc, o, lse, ws);
   });
 }

@@ -1,5 +1,8 @@
 """The serving operators' calls from Python on CUDA tensors: what the ordinary
-call refuses and raises."""
+call refuses, raises and leaves to other threads."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -92,3 +95,41 @@ def test_a_choice_without_a_truth_value_raises_its_own_error(S):
                  lambda: S.pa_paged_append(q, k, k, row, row, pages[0], pages[1], rope_theta=1e4, want_k=Undecided())):
         with pytest.raises(KeyError, match="neither"):
             call()
+
+
+def test_other_threads_run_while_launches_wait(S):
+    # the GPU is busy for a second, the queue of launches fills, and a call waits
+    # in the launch: not with the interpreter's lock
+    lens, table, free = i32([1, 1]), i32([[0, 0], [1, 1]]), i32([5, 6])
+    q, k = randn((2, 4, 64), torch.bfloat16, 1), randn((2, 2, 64), torch.bfloat16, 2)
+    pages = torch.zeros((2, 2, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    cu, slots = i32([0, 1, 2]), i32([0, 16])
+    calls = (lambda: S.pa_paged_schedule(lens, lens, table, free, 16, 2),
+             lambda: S.pa_paged_append(q, k, k, lens, slots, pages[0], pages[1], rope_theta=1e4),
+             lambda: S.pa_prompt_attend(q, k, k, cu),
+             lambda: S.pa_paged_attend(q, cu, lens, table, pages[0], pages[1], 1))
+    for call in calls:
+        for _ in range(3):
+            call()
+        torch.cuda.synchronize()
+        stop, gaps = threading.Event(), [0.0]
+
+        def tick():
+            last = time.perf_counter()
+            while not stop.is_set():
+                time.sleep(0.002)
+                now = time.perf_counter()
+                gaps.append(now - last)
+                last = now
+        thread = threading.Thread(target=tick)
+        thread.start()
+        torch.cuda._sleep(2_000_000_000)
+        begin = time.perf_counter()
+        for _ in range(2500):
+            call()
+        waited = time.perf_counter() - begin
+        stop.set()
+        thread.join()
+        torch.cuda.synchronize()
+        assert waited > 0.4, "no launch had to wait"
+        assert max(gaps) < 0.2, f"another thread stood still for {max(gaps):.2f} of {waited:.2f} s"
