@@ -1,7 +1,7 @@
 """Build step of the native library: compiles csrc/*.cu for sm_100a into
 ``libpulsar_b200.so`` beside this file (in-tree, so it travels with the
 source tree), and the serving operators' Python call layer (csrc/*.cpp, against
-torch's headers) into ``_serving_call.so``.  Runs on a machine without a GPU:
+torch's headers) into ``call_layer_path()``.  Runs on a machine without a GPU:
 nvcc cross-compiles.
 
     python -m long_context_blockwise_max_b200.build [--force] [--verbose]
@@ -19,7 +19,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libpulsar_b200.so")
 CALL_SRC = os.path.join(CSRC, "serving_call.cpp")
-CALL = os.path.join(PKG, "_serving_call.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -51,13 +50,23 @@ def _compile(src: str, obj: str, ptxas_verbose: bool) -> subprocess.CompletedPro
     return subprocess.run(cmd, capture_output=True, text=True)
 
 
+def call_layer_path() -> str:
+    """The call layer built for this Python and this torch: it uses both by
+    their binary interfaces, which no other version need share."""
+    import sysconfig
+
+    import torch
+    return os.path.join(PKG, f"_serving_call.torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_call_layer(force: bool = False) -> str:
-    """Compile the Python call layer of the serving operators if a source or
-    header of it is newer; return its path.  Links to the library built by
-    ``build`` (found beside it at run time)."""
+    """Compile the Python call layer of the serving operators if there is none
+    for this Python and torch, or a source or header of it is newer; return its
+    path.  Links to the library built by ``build`` (found beside it at run time)."""
+    call = call_layer_path()
     deps = [CALL_SRC] + glob.glob(os.path.join(ROOT, "include", "*.h"))
-    if not force and os.path.exists(CALL) and all(os.path.getmtime(p) <= os.path.getmtime(CALL) for p in deps):
-        return CALL
+    if not force and os.path.exists(call) and all(os.path.getmtime(p) <= os.path.getmtime(call) for p in deps):
+        return call
     import sysconfig
 
     import torch
@@ -65,7 +74,7 @@ def build_call_layer(force: bool = False) -> str:
     inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
     lib = os.path.join(base, "lib")
-    tmp = CALL + ".tmp"
+    tmp = call + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in inc), CALL_SRC,
            "-o", tmp, f"-L{PKG}", "-l:" + os.path.basename(LIB), f"-L{lib}", "-ltorch_python", "-ltorch_cuda",
@@ -74,8 +83,8 @@ def build_call_layer(force: bool = False) -> str:
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("compiling the call layer failed")
-    os.replace(tmp, CALL)
-    return CALL
+    os.replace(tmp, call)
+    return call
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:

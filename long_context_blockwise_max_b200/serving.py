@@ -20,17 +20,28 @@ the compiled call layer ``_serving_call``, which does the same in less time.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 from functools import lru_cache
 
 import torch
 
-from . import pulsar
+from . import build, pulsar
 from .pulsar import PulsarError, _check, _dtype_code, _lib, _need, _same
 
-try:
-    from . import _serving_call as _ordinary
-except ImportError as e:
-    raise ImportError(f"{e}; run `python -m long_context_blockwise_max_b200.build`") from e
+
+
+def _load_call_layer():
+    path = build.call_layer_path()
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is not built; run `python -m long_context_blockwise_max_b200.build`")
+    spec = importlib.util.spec_from_file_location(f"{__package__}._serving_call", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_ordinary = _load_call_layer()
 
 # Every symbol declared in include/pulsar_serving.h.
 ABI_SYMBOLS = (
