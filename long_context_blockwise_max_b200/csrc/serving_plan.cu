@@ -455,11 +455,13 @@ size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws) {
     a.piece_cost = a.tile_rows == 16 ? 1.f : 0.3f;
     a.merge_cost = a.tile_rows == 16 ? 2.f : 0.6f;
   }
-  // Rows per kv head up to which a request is the decode kernel's.  A call
-  // whose requests are long on average leaves them all to the tile kernel:
-  // its few short ones cost less there than another launch.
+  // Rows per kv head up to which a request is the decode kernel's, in calls
+  // that may have such a request: a token has no more rows than that, and either
+  // every request is that short or N < B * max_q says that some has fewer than
+  // max_q tokens.  (N counts padding rows too: a batch padded to B * max_q rows is
+  // the tile kernel's as a whole.)
   a.small_rows = 0;
-  if (a.dtype == PA_BF16 && a.max_q > 0 &&
+  if (a.dtype == PA_BF16 && a.max_q > 0 && g <= kDecodeRows &&
       (static_cast<int64_t>(a.max_q) * g <= kDecodeRows || a.N < static_cast<int64_t>(a.B) * a.max_q))
     a.small_rows = kDecodeRows;
   a.decode_ctas = a.small_rows > 0 ? kSms : 0;
