@@ -94,14 +94,15 @@ struct Cursor {
 
   __device__ __forceinline__ void load(const AttendArgs& a) {
     row0 = a.cu_q[b];
-    q = a.cu_q[b + 1] - row0;
+    const int64_t rows = static_cast<int64_t>(a.cu_q[b + 1]) - row0;
+    q = rows > 0 && rows <= a.max_q ? static_cast<int>(rows) : 0;
     kv = a.kv_len[b];
-    n_units = kv > 0 ? (kv + kPlanTile - 1) / kPlanTile : 1;
+    n_units = kv > 0 ? (kv - 1) / kPlanTile + 1 : 1;   // (kv may be as large as the type allows)
   }
   // requests that are not this kernel's (or were found invalid by the plan)
   // have no groups; the caller steps at most as many times as there are groups
   __device__ __forceinline__ bool mine(const AttendArgs& a, int64_t max_kv) const {
-    return row0 >= 0 && q > 0 && q <= a.max_q && static_cast<int64_t>(row0) + q <= a.N && kv >= 0 && kv <= max_kv &&
+    return row0 >= 0 && q > 0 && static_cast<int64_t>(row0) + q <= a.N && kv >= 0 && kv <= max_kv &&
            static_cast<int64_t>(q) * (a.hq / a.hkv) <= a.small_rows;
   }
   __device__ __forceinline__ void step(const AttendArgs& a, int64_t max_kv) {

@@ -198,8 +198,10 @@ __device__ __forceinline__ bool get_item(const SvBars* bars, int k, Item& it) {
 __device__ __forceinline__ void put_item(SvBars* bars, int k, int tpt, const Piece& pc, int kvh) {
   const int ctx = pc.kv_len - pc.q_len, n = pc.kt1 - pc.kt0;
   const bool two = pc.tok0 + tpt < pc.q_len;
-  const int seen = max(0, ctx + pc.tok0 + tpt);    // keys that tile 0 sees (it is full)
-  const int nt0 = two ? max(0, min(n, (seen + kKeyTile - 1) / kKeyTile - pc.kt0)) : (n + 1) / 2;
+  // keys that tile 0 sees (it is full); with a tile's more they may pass 2^31
+  const int64_t seen = keys_seen(pc.kv_len, pc.q_len, static_cast<int64_t>(pc.tok0) + tpt);
+  const int deep = static_cast<int>((seen + kKeyTile - 1) / kKeyTile);
+  const int nt0 = two ? max(0, min(n, deep - pc.kt0)) : (n + 1) / 2;
   bars->work[k & 1].rows = make_int4(pc.row0, pc.tok0, pc.q_len, pc.kv_len);
   bars->work[k & 1].keys = make_int4(pc.kt0, n, pc.part, kvh);
   bars->work[k & 1].tiles = make_int4(nt0, two ? n : n / 2, max(0, max(0, ctx + pc.tok0 + 1) / kKeyTile - pc.kt0),

@@ -1,9 +1,11 @@
 """Serving attention on the GPU with values at the border of what can be
-weighed: infinite V behind scores that are far apart."""
+weighed or counted: infinite V behind scores that are far apart, caches as
+long as a table allows."""
 import pytest
 import torch
 
-from serving_cases import DTYPES, paged_batch
+from oracle import serving_oracle as so
+from serving_cases import DTYPES, check_rows, paged_batch
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +48,39 @@ def test_a_visible_infinity_with_a_vanishing_weight_is_not_lost(S, dtype, q_len,
     keep[:, :4, 5:7] = False
     keep[:, 4:, 7] = False
     assert torch.equal(o[keep], o0[keep])
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1, 2], [3, 1, 40]], ids=["decode", "chunk"])
+def test_a_cache_as_long_as_a_table_allows(S, q_lens):
+    # 2^31 - 16 keys: one page of zeros, many times over, then one of ordinary
+    # keys, whose scores weigh by e^40 more than all the others.  The long request
+    # comes last, behind short ones.
+    hq, hkv, d, page = 8, 1, 64, 16
+    width = (2 ** 31 - 1) // page
+    kv_lens = [5, 0, width * page]
+    table = torch.zeros((3, width), dtype=torch.int32, device="cuda")
+    table[2, -4:] = torch.arange(1, 5, device="cuda")
+    table[0, 0] = 5
+    k, v = (torch.zeros((6, page, hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    gen = torch.Generator().manual_seed(4)
+    k[1:, :, :, 0] = 64.0      # 64 * 8 / sqrt(64) = 64 above the zeros' score; 2^31 of them weigh e^(21.5 - 64)
+    k[1:] += torch.randn((5, page, hkv, d), generator=gen).to(k)
+    v[1:] = torch.randn((5, page, hkv, d), generator=gen).to(v)
+    n = sum(q_lens)
+    q = torch.randn((n, hq, d), generator=gen).to(v)
+    q[:, :, 0] = 8.0
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    cu = torch.tensor([0, q_lens[0], q_lens[0] + q_lens[1], n], dtype=torch.int32, device="cuda")
+    kv = torch.tensor(kv_lens, dtype=torch.int32, device="cuda")
+    o, lse, ws = S.pa_paged_attend(q, cu, kv, table, k, v, max(q_lens))
+    assert ok(S, ws) == 0
+    qh, kh, vh = (t.double().cpu().numpy() for t in (q, k, v))
+    at = 0
+    for b, (m, row, keys) in enumerate(zip(q_lens, ([5], [], [1, 2, 3, 4]), (5, 0, 64))):
+        if m and keys:
+            kk, vv = (x[row].reshape(-1, hkv, d)[:keys] for x in (kh, vh))
+            want = so.attend_rows(qh[at:at + m], kk, vv, keys - m)
+            check_rows(torch.bfloat16, o[at:at + m], lse[at:at + m], want, keys, f"request {b}")
+        elif m:
+            assert (o[at:at + m] == 0).all() and torch.isneginf(lse[at:at + m]).all()
+        at += m
