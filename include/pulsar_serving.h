@@ -127,7 +127,10 @@ size_t pa_prompt_attend_workspace_size(int32_t B, int64_t N, int32_t hq, int32_t
  * for the product with V (one rounding, half a step of 2^-7 relative; the
  * row sum is taken before it); one rounding of o.
  * A masked key adds nothing whatever its K and V hold (infinities and NaN
- * included); a visible non-finite V makes that column of o non-finite.
+ * included); a visible non-finite V makes that column of o non-finite (the
+ * infinity, or NaN).  A visible key whose score is -inf weighs nothing, and a
+ * row all of whose keys are such counts as one that sees no key: lse = -inf and,
+ * where V is finite, o = 0.
  */
 int pa_prompt_attend(const void* q, const void* k, const void* v, int dtype, int64_t N, int64_t ldq,
                      int64_t ldk, int64_t ldv, const int32_t* cu_q, int32_t B, int32_t hq,

@@ -1,11 +1,13 @@
 """Serving attention on the GPU with values at the border of what can be
-weighed or counted: infinite V behind scores that are far apart, caches as
-long as a table allows."""
+weighed or counted: infinite V behind scores that are far apart, scores of
+-inf, caches as long as a table allows, K and V too large for L2 (another order
+of work)."""
+import numpy as np
 import pytest
 import torch
 
 from oracle import serving_oracle as so
-from serving_cases import DTYPES, check_rows, paged_batch
+from serving_cases import DTYPES, check_rows, paged_batch, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -50,6 +52,28 @@ def test_a_visible_infinity_with_a_vanishing_weight_is_not_lost(S, dtype, q_len,
     assert torch.equal(o[keep], o0[keep])
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("q_len,kv_len", [(1, 60), (1, 9000), (4, 9000), (40, 300), (40, 9000), (150, 400)])
+def test_scores_of_minus_infinity(S, dtype, q_len, kv_len):
+    # a key whose score is -inf weighs nothing; a row all of whose keys are such
+    # counts as one that sees no key, whichever kernel has it
+    c = paged_batch([q_len], [kv_len], 8, 2, 64, 16, DTYPES[dtype], seed=q_len, poison=False)
+    q, k = c["q"].abs() + 0.5, c["k_pages"].clone()
+    args = lambda k: (q, c["cu_q"], c["kv_len"], c["table"], k, c["v_pages"], q_len)
+    k[:, :, 0] = -float("inf")
+    o, lse, ws = S.pa_paged_attend(*args(k))
+    assert ok(S, ws) == 0
+    assert (o[:, :4] == 0).all() and torch.isneginf(lse[:, :4]).all()
+    o0, lse0, _ = S.pa_paged_attend(*args(c["k_pages"]))
+    assert torch.equal(o[:, 4:], o0[:, 4:]) and torch.equal(lse[:, 4:], lse0[:, 4:])
+    # all but the first key: every row's answer is its V
+    page = int(c["table"][0, 0])
+    k[page, 0, 0] = 0.0
+    o, lse, ws = S.pa_paged_attend(*args(k))
+    assert ok(S, ws) == 0 and (lse[:, :4] == 0).all()
+    assert (o[:, :4] == c["v_pages"][page, 0, 0]).all()
+
+
 @pytest.mark.parametrize("q_lens", [[1, 1, 2], [3, 1, 40]], ids=["decode", "chunk"])
 def test_a_cache_as_long_as_a_table_allows(S, q_lens):
     # 2^31 - 16 keys: one page of zeros, many times over, then one of ordinary
@@ -84,3 +108,53 @@ def test_a_cache_as_long_as_a_table_allows(S, q_lens):
         elif m:
             assert (o[at:at + m] == 0).all() and torch.isneginf(lse[at:at + m]).all()
         at += m
+
+
+def spread_rows(n, count):
+    """The ends of a sequence, and rows of it at about equal distances."""
+    return sorted({0, n - 1} | {int(x) for x in np.linspace(0, n - 1, count)})
+
+
+@pytest.mark.parametrize("lens", [[32768], [20001, 9000, 1, 5000]], ids=["one", "several"])
+def test_prompts_beyond_the_cache(S, lens):
+    # 134 MB and more of K and V in more than two waves of pieces per kv head:
+    # the pieces of one kv head run together, where shorter calls take all heads
+    # in order of depth.  Rows spread over each prompt against 64 bits.
+    n, hq, hkv, d = sum(lens), 32, 8, 128
+    q, k, v = (randn((n, h, d), torch.bfloat16, 70 + i) for i, h in enumerate((hq, hkv, hkv)))
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    o, lse, ws = S.pa_prompt_attend(q, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    assert ok(S, ws) == 0 and torch.isfinite(o).all() and torch.isfinite(lse).all()
+    for b, m in enumerate(lens):
+        kh, vh = (t[cu[b]:cu[b + 1]].double().cpu().numpy() for t in (k, v))
+        for i in spread_rows(m, 8):
+            row = slice(cu[b] + i, cu[b] + i + 1)
+            want = so.attend_rows(q[row].double().cpu().numpy(), kh[:i + 1], vh[:i + 1], i)
+            check_rows(torch.bfloat16, o[row], lse[row], want, i + 1, f"prompt {b}, row {i}")
+
+
+def test_paged_chunks_beyond_the_cache(S):
+    # the same order of work over pages: two chunks behind long caches
+    q_lens, kv_lens, hq, hkv, d = [9000, 12000], [20000, 17000], 32, 8, 128
+    page, n = 64, 21000
+    n_pages = sum(-(-kv // page) for kv in kv_lens)
+    k, v = (randn((n_pages, page, hkv, d), torch.bfloat16, 80 + i) for i in range(2))
+    q = randn((n, hq, d), torch.bfloat16, 82)
+    order = np.random.default_rng(8).permutation(n_pages)
+    table = np.zeros((2, max(-(-kv // page) for kv in kv_lens)), dtype=np.int64)
+    at = 0
+    for b, kv in enumerate(kv_lens):
+        held = -(-kv // page)
+        table[b, :held] = order[at:at + held]
+        at += held
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    o, lse, ws = S.pa_paged_attend(q, i32([0, 9000, 21000]), i32(kv_lens), i32(table), k, v, 12000)
+    assert ok(S, ws) == 0 and torch.isfinite(o).all() and torch.isfinite(lse).all()
+    kh, vh = (t.float().cpu().numpy() for t in (k, v))
+    for b, (m, kv) in enumerate(zip(q_lens, kv_lens)):
+        keys, vals = (so.paged_keys(x, table[b], kv).astype(np.float64) for x in (kh, vh))
+        lo = 9000 * b
+        for i in spread_rows(m, 6):
+            row, seen = slice(lo + i, lo + i + 1), kv - m + i + 1
+            want = so.attend_rows(q[row].double().cpu().numpy(), keys[:seen], vals[:seen], seen - 1)
+            check_rows(torch.bfloat16, o[row], lse[row], want, seen, f"chunk {b}, row {i}")
