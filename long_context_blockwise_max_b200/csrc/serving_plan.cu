@@ -27,8 +27,18 @@ constexpr int kCuts = 32;
 constexpr int kMaxCut = 64;
 constexpr int kMaxCutItems = 1024;
 // key tiles of 2.1 us per block.  32 requests, four of them tokens behind up to
-// 27 keys: 108 us with the decode kernel at work, 97 us without.
+// 27 keys: 108 us with the decode kernel at work, 97 us without.  (The border lies
+// low: beside five chunks of 256 over 8000 keys, 4 tokens over 1000, 2.8 tiles, take
+// 285 / 265 us with and without, and 8 of them, 5.6 tiles, still 294 / 264.)
 constexpr int kFewTiles = 3;
+// ... and, where the chunks' pieces fit one wave of blocks, as long as blocks stay
+// for the parts that their keys are cut into: this many key tiles per block at most
+// may move from the few tokens' blocks to the others.  Chunks of 256 over 8000 keys,
+// 32 / 8 heads, with tokens over 64 keys, decode kernel / tiles: one chunk with 2 or 8
+// tokens (moves 2, 10) 65 / 61, 67 / 87 us; two with 2 or 8 (3, 21) 109 / 101, 110 / 113;
+// three with 2 or 4 (5, 11) 148 / 145, 149 / 145; four with 2 or 4 (7, 15) 161 / 157,
+// 159 / 190 us.
+constexpr int kFewMoved = 9;
 // K and V of this many bytes stay in L2 (126 MB) beside q and o.  Pieces of
 // more, but of no more than two waves per head, are also taken over all heads
 // in order of depth: a balanced end is worth more than the reuse.
@@ -81,7 +91,9 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
   __shared__ int hist[kBuckets];
   __shared__ int depth[kMaxCutItems], part_of[kMaxCutItems], first_piece[kMaxCutItems + 1];
   __shared__ int deepest, n_merge;
-  __shared__ int few[3];   // deepest chunk, deepest request of few rows, key tiles of those
+  // deepest chunk, deepest request of few rows, key tiles of those; pieces of the
+  // chunks, their key tiles, requests of few rows
+  __shared__ int few[6];
   __shared__ unsigned key_tiles;
   __shared__ int cost_pieces[kCuts], cost_cuts[kCuts], cost_load[kCuts], best;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
@@ -96,36 +108,52 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     key_tiles = 0;
   }
   if (tid < kCuts) cost_pieces[tid] = cost_cuts[tid] = cost_load[tid] = 0;
-  if (tid < 3) few[tid] = 0;
+  if (tid < 6) few[tid] = 0;
   __syncthreads();
   // Few generated tokens with short caches beside chunks: the decode kernel
   // takes 8 us whatever it has to do, and 2 us for nothing.  They are the tile
-  // kernel's when its blocks need less for them (kFewTiles key tiles each) and
-  // no cache is longer than the chunks' longest.
+  // kernel's when its blocks need less for them (kFewTiles key tiles each), no
+  // cache is longer than the chunks' longest, and they take no blocks that the
+  // chunks' keys need (kFewMoved).  (Sums are kept below 2^30 by clamps that only
+  // calls of many waves reach.)
   int small_rows = a.small_rows;
   if (a.tiles && small_rows > 0) {
-    int cost = 0, deep_small = 0, deep = 0;
+    constexpr int kMost = 1 << 20;
+    int cost = 0, deep_small = 0, deep = 0, pieces = 0, tiles = 0, tokens = 0;
     for (int b = tid; b < a.B; b += threads) {
       const Lens r = lens_of(a, b, max_kv, false);
       if (r.q <= 0) continue;
       const int d = static_cast<int>((r.kv + kPlanTile - 1) / kPlanTile);
       if (r.rows > small_rows) {
+        const int64_t n = (static_cast<uint32_t>(r.q) + a.tile_tokens - 1) / static_cast<uint32_t>(a.tile_tokens);
         deep = max(deep, d);
+        pieces = static_cast<int>(min(pieces + n, static_cast<int64_t>(kMost)));
+        tiles = static_cast<int>(min(tiles + n * d, static_cast<int64_t>(kMost)));
       } else {
         deep_small = max(deep_small, d);
-        cost = min(cost + d + static_cast<int>(a.piece_cost), 1 << 20);
+        cost = min(cost + d + static_cast<int>(a.piece_cost), kMost);
+        ++tokens;
       }
     }
     deep = __reduce_max_sync(0xffffffffu, deep);
     deep_small = __reduce_max_sync(0xffffffffu, deep_small);
     cost = __reduce_add_sync(0xffffffffu, cost);
+    pieces = __reduce_add_sync(0xffffffffu, pieces);
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    tokens = __reduce_add_sync(0xffffffffu, tokens);
     if (lane == 0) {
       atomicMax(&few[0], deep);
       atomicMax(&few[1], deep_small);
-      atomicAdd(&few[2], min(cost, 1 << 20));
+      atomicAdd(&few[2], min(cost, kMost));
+      atomicAdd(&few[3], min(pieces, kMost));
+      atomicAdd(&few[4], min(tiles, kMost));
+      atomicAdd(&few[5], tokens);
     }
     __syncthreads();
-    if (few[1] <= few[0] && static_cast<int64_t>(few[2]) * a.hkv <= kFewTiles * a.slots) small_rows = 0;
+    if (few[1] <= few[0] && static_cast<int64_t>(few[2]) * a.hkv <= kFewTiles * a.slots) {
+      const int64_t h = a.hkv, blocks = few[3] * h, taken = few[5] * h, left = a.slots - taken;
+      if (blocks > a.slots || (left > 0 && few[4] * h * taken <= kFewMoved * a.slots * left)) small_rows = 0;
+    }
   }
   int64_t item_base = 0, unit_base = 0;
   for (int b0 = 0; b0 < a.B; b0 += threads) {
