@@ -23,6 +23,13 @@ constexpr int kBuckets = 256;
 // be alone at the end.  512 tokens over 128K keys beside 64 x 128 over 1K: 1960 us
 // whole, 1076 us cut; looking in vain costs 3 us).
 constexpr int kPromptWaves = 3, kPagedWaves = 16;
+// From three waves on, a cut has to promise a tenth: what it costs there is
+// underrated.  512 tokens over 8K / 32K / 128K keys beside m x 128 over 1K, whole / cut, and
+// the promise: m = 40 193 / 213 (5 %), 538 / 424 (30 %), 1967 / 1212 us (74 %);
+// m = 64 237 / 272 (1 %), 537 / 476 (15 %), 1970 / 1262 (72 %); m = 140 439 / 457 (0),
+// 638 / 720 (3 %), 2042 / 1537 (52 %).  (Beyond 16 waves it is not looked at: m = 200
+// 642 / 647, 1031 / 898, 2462 / 1749.)
+constexpr float kCutMargin = 0.9f;
 constexpr int kCuts = 32;
 constexpr int kMaxCut = 64;
 constexpr int kMaxCutItems = 1024;
@@ -260,6 +267,7 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
           cost = fmaxf(cost, (cost_load[lane] + a.piece_cost * cost_pieces[lane]) * a.hkv / a.slots +
                                  0.5f * piece * fminf(1.f, 3.f * a.slots / blocks));
         if (cuts > 1) cost += a.merge_cost * (1.f + cuts / 24.f);
+        else if (blocks >= static_cast<int64_t>(kPromptWaves) * a.slots) cost *= kCutMargin;
         if (cost_cuts[lane] > a.part_cap || cuts > deepest) cost = INFINITY;
         const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));
         const unsigned who = __ballot_sync(0xffffffffu, __float_as_uint(cost) == least);

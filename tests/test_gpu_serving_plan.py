@@ -47,3 +47,11 @@ def test_few_tokens_take_no_blocks_that_the_chunks_need(S, chunks, tokens, tiles
         assert both[0] - both[1] >= tokens and both[0] > whole
     else:
         assert both == alone
+
+
+@pytest.mark.parametrize("others,keys,cut", [(40, 8192, False), (40, 32768, True), (64, 8192, False), (64, 32768, True),
+                                             (140, 32768, False), (140, 131072, True)])
+def test_among_many_rows_a_cut_has_to_promise_enough(S, others, keys, cut):
+    pieces, groups, _ = plan_of(S, [512] + [128] * others, [keys] + [1024] * others)
+    assert pieces >= 8 + 2 * others
+    assert (groups > 0) == cut
