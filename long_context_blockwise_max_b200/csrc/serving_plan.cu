@@ -46,10 +46,17 @@ constexpr int kFewTiles = 3;
 // three with 2 or 4 (5, 11) 148 / 145, 149 / 145; four with 2 or 4 (7, 15) 161 / 157,
 // 159 / 190 us.
 constexpr int kFewMoved = 9;
-// K and V of this many bytes stay in L2 (126 MB) beside q and o.  Pieces of
-// more, but of no more than two waves per head, are also taken over all heads
-// in order of depth: a balanced end is worth more than the reuse.
+// K and V of this many bytes stay in L2 (126 MB) beside q and o, and pieces are taken
+// over all heads in order of depth (24 prompts of 1 to 4096 tokens: 162 us, by heads
+// 175).  Beyond, a head's pieces share its keys in L2 (8 x 4096 tokens, 134 MB: 1168 us by
+// heads, 1247 over all of them; at 50 to 100 MB both within 2 %), unless they are so
+// uneven that the last head's deepest piece would end alone: with at most two waves
+// per head, and the deepest at least kUneven times the average.  32 mixed requests
+// over up to 8K keys (128 MB) 97 us over all heads, 111 by heads; 2048 tokens each over
+// 64K / 1 .. 64K / 4 keys 4.15 to 4.26 / 4.34 to 4.37 ms; but 8 x 2048 over 32K 9.0 to 9.3 /
+// 8.14 ms, 4 x 2048 over 32K 4.23 to 4.30 / 4.03, and 16384 over 32K 6.2 / 6.1.
 constexpr double kL2Keys = 100e6;
+constexpr float kUneven = 1.5f;
 
 struct Lens {
   int64_t row0, q, kv;
@@ -102,6 +109,7 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
   // chunks, their key tiles, requests of few rows
   __shared__ int few[6];
   __shared__ unsigned key_tiles;
+  __shared__ unsigned long long piece_tiles;   // of all pieces, about
   __shared__ int cost_pieces[kCuts], cost_cuts[kCuts], cost_load[kCuts], best;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   if (tid < static_cast<int>(kStatusBytes / 4)) reinterpret_cast<int32_t*>(a.status)[tid] = 0;
@@ -113,6 +121,7 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     deepest = 0;
     n_merge = 0;
     key_tiles = 0;
+    piece_tiles = 0;
   }
   if (tid < kCuts) cost_pieces[tid] = cost_cuts[tid] = cost_load[tid] = 0;
   if (tid < 6) few[tid] = 0;
@@ -167,6 +176,7 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     const int b = b0 + tid;
     int64_t ni = 0, nu = 0;
     int depth_b = 0;
+    unsigned tiles_b = 0;
     if (b < a.B) {
       const Lens r = lens_of(a, b, max_kv, true);
       if (r.q > 0) {
@@ -176,15 +186,20 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
         } else {
           ni = (static_cast<uint32_t>(r.q) + a.tile_tokens - 1) / static_cast<uint32_t>(a.tile_tokens);
           depth_b = static_cast<int>((r.kv + kPlanTile - 1) / kPlanTile);
+          // (its average piece sees the keys before half of its tokens)
+          const int64_t t = ni * (keys_seen(r.kv, r.q, r.q / 2) + kPlanTile - 1) / kPlanTile;
+          tiles_b = static_cast<unsigned>(min(t, static_cast<int64_t>(1 << 26)));
         }
       }
     }
     depth_b = max(depth_b, 0);
     const int warp_deepest = __reduce_max_sync(0xffffffffu, depth_b);
     const unsigned warp_tiles = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(depth_b));
+    const unsigned warp_piece_tiles = __reduce_add_sync(0xffffffffu, tiles_b);
     if (lane == 0 && warp_deepest > 0) {
       atomicMax(&deepest, warp_deepest);
       atomicAdd(&key_tiles, warp_tiles);
+      atomicAdd(&piece_tiles, static_cast<unsigned long long>(warp_piece_tiles));
     }
     int64_t i_all, u_all;
     block_incl_scan2<int64_t>(ni, nu, tmp[(b0 / threads) & 1], &i_all, &u_all);
@@ -379,7 +394,8 @@ __global__ void __launch_bounds__(1024) attend_plan_kernel(AttendArgs a, int64_t
     a.head->abort = 0;
     a.head->next = 0;
     const double kv_bytes = static_cast<double>(key_tiles) * kPlanTile * a.hkv * a.d * (a.dtype == PA_BF16 ? 4 : 8);
-    a.head->heads_inner = kv_bytes <= kL2Keys || n_pieces <= 2 * a.slots;
+    const bool uneven = static_cast<float>(deepest) * item_base >= kUneven * static_cast<float>(piece_tiles);
+    a.head->heads_inner = kv_bytes <= kL2Keys || (n_pieces <= 2 * a.slots && uneven);
   }
 }
 

@@ -55,3 +55,10 @@ def test_among_many_rows_a_cut_has_to_promise_enough(S, others, keys, cut):
     pieces, groups, _ = plan_of(S, [512] + [128] * others, [keys] + [1024] * others)
     assert pieces >= 8 + 2 * others
     assert (groups > 0) == cut
+
+
+@pytest.mark.parametrize("q,kv,inner", [([2048] * 8, [32768] * 8, 0), ([2048] * 4, [65536, 32768, 21845, 16384], 1),
+                                        ([16384], [32768], 0), ([64, 64, 200, 1000], [20000, 4000, 300, 8000], 1)])
+def test_even_pieces_of_a_head_share_its_keys(S, q, kv, inner):
+    # beyond what L2 holds (or below it: the last case), in no more than two waves a head
+    assert plan_of(S, q, kv)[2] == inner
