@@ -33,8 +33,12 @@
 // tensor pipe and the exponentials are each 54 % busy; TMEM has no room for a
 // second S.  A piece's output takes another 3800 (64 KB out of one SM).  32 / 8
 // heads of 128: one 32K prompt 8.0 to 8.2 ms = 1070 to 1100 TFLOP/s at the power
-// cap (7.0 ms before it sets in); 24 prompts of 1 to 4096 tokens 160 us; a 64-token
-// query over 128K keys 170 to 180 us with its plan and merge.
+// cap (7.0 ms before it sets in); 24 prompts of 1 to 4096 tokens 160 to 165 us; a
+// 64-token query over 128K keys 168 to 181 us with its plan and merge.
+//
+// P is rounded to bf16 (half a step, 2^-8 of each probability; the row sum is taken
+// before it), as its product with V needs: a second product with the residual would
+// add half of the tensor pipe's work, and TMEM has no columns for it.
 //
 // Guard: P is zero at a masked key, but zero times an infinity or NaN in its
 // V is NaN.  In tiles with keys that some row does not see, rows past the
@@ -43,8 +47,9 @@
 // the epilogue gives rows that do see it the value the sum would have.
 //
 // Every wait on an mbarrier is bounded; on expiry the block records
-// PA_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and returns.  No
-// barrier runs more than one phase ahead of a waiter: those that a role could
+// PA_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and returns.  (A wait may
+// last as long as a piece, so its limit grows with the deepest that the arguments
+// allow.)  No barrier runs more than one phase ahead of a waiter: those that a role could
 // pass a whole piece early come in pairs, used in turn.
 #include <cudaTypedefs.h>
 
@@ -778,6 +783,10 @@ int launch_tc(const AttendArgs& a, cudaStream_t s) {
   const int g = a.hq / a.hkv;
   SvParams p;
   p.a = a;
+  // roles wait for one another for up to a piece: 10 us for each of its key tiles,
+  // which take 2 us (0.01 s for 128K keys)
+  const int64_t deepest = PAGED ? static_cast<int64_t>(a.max_pages) * a.page_size : a.N;
+  p.a.wait_limit_ns += static_cast<uint64_t>(deepest / kKeyTile) * 10000u;
   p.box_rows = PAGED && a.page_size < kKeyTile ? a.page_size : kKeyTile;
   // an empty cache has no page to read: every box is out of range, and the
   // map is made over q only to have an address

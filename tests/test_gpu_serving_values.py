@@ -110,6 +110,22 @@ def test_a_cache_as_long_as_a_table_allows(S, q_lens):
         at += m
 
 
+def test_a_piece_may_last_longer_than_a_wait_between_tiles(S):
+    # more kv heads than cuts are made for: each piece has all of 200 million keys,
+    # 1.8 s of work.  Equal scores.
+    hkv, d, page, width, m = 152, 64, 1024, 200_000, 20
+    k = torch.zeros((1, page, hkv, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.ones_like(k)
+    q = torch.ones((m, hkv, d), dtype=torch.bfloat16, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    table = torch.zeros((1, width), dtype=torch.int32, device="cuda")
+    o, lse, ws = S.pa_paged_attend(q, i32([0, m]), i32([width * page]), table, k, v, m)
+    assert ok(S, ws) == 0
+    assert torch.isfinite(o).all()
+    keys = torch.arange(width * page - m + 1, width * page + 1, dtype=torch.float64)
+    assert (lse.double().cpu() - keys.log()[:, None]).abs().max() <= 1e-4
+
+
 def spread_rows(n, count):
     """The ends of a sequence, and rows of it at about equal distances."""
     return sorted({0, n - 1} | {int(x) for x in np.linspace(0, n - 1, count)})
