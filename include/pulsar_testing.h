@@ -48,8 +48,8 @@ int pa_testing_phase2_stall(const void* q, const void* k_ret, const void* v_ret,
  * device wait limited to wait_limit_us microseconds (1 .. 10^7) and one barrier
  * per block made unsatisfiable in the same way: the Q barrier of the tile
  * kernel (max_q * hq / hkv > 16), each warp's first key copy in the decode
- * kernel.  Every block records PA_ERR_TIMEOUT, drains its copies and MMAs and
- * returns; the context stays usable.  Arguments as pa_paged_attend (lse not
+ * kernel.  Every block that has work records PA_ERR_TIMEOUT, drains its copies and
+ * MMAs and returns; the context stays usable.  Arguments as pa_paged_attend (lse not
  * written); the outputs are unspecified.
  */
 int pa_testing_paged_stall(const void* q, int64_t N, const int32_t* cu_q, const int32_t* kv_len, int32_t B,

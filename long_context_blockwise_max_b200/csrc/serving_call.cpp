@@ -5,8 +5,9 @@
 // ordinary call what serving.py does for every call: check the tensors,
 // allocate the outputs and the workspace, and pass raw pointers and the
 // current stream to the C entry point.  Whatever is not plainly an ordinary
-// call (another device, an unusual stride, a wrong type) returns None, and
-// serving.py takes it from there, with its own checks and messages.
+// call (another device, an unusual stride, a wrong type, pages or a table over
+// what the call reads) returns None, and serving.py takes it from there, with its
+// own checks and messages.
 //
 // Each returns a tuple of tensors (the last one is the workspace), a negative
 // pa_status as an int, or None.
@@ -56,7 +57,7 @@ struct Args {
     if (t && (t->scalar_type() != at::kInt || !t->is_contiguous() || t->numel() < count)) ok = false;
     return t;
   }
-  // packed [N][heads][d] rows, N > 1, dense inside a token
+  // packed [N][heads][d] rows, N >= 1, dense inside a token
   const Tensor* rows(int i, int64_t* ld) {
     const Tensor* t = tensor(i);
     if (!t) return nullptr;

@@ -27,8 +27,9 @@ int clear_status(DeviceStatus* status, cudaStream_t s) {
 // Two prefix sums over the requests (new tokens, new pages), then one entry
 // per token and per new page, each found by bisection in them.  Every block
 // builds the sums by itself (B is at most 8192: a few loads per thread that
-// hit L2), which saves a second launch and a grid-wide wait; tokens and pages
-// are spread over the blocks.  Latency-bound: 64 requests with a token each
+// hit L2), which saves a kernel for them and a grid-wide wait; tokens and pages
+// are spread over the blocks.  A step of one block is one launch, one of more has
+// its status cleared by another before it.  Latency-bound: 64 requests with a token each
 // take 2.8 us in a graph (their loads, one scan and one look-up), 512 requests
 // with 150K tokens 5.5 us.
 __global__ void __launch_bounds__(1024) paged_schedule_kernel(ScheduleArgs a) {

@@ -4,10 +4,10 @@
 // The lengths are on the device, so the plan is made there, by one block,
 // in the call itself: a list of pieces for the tile kernels (one per group
 // of rows, the deepest first, so that the short ones fill the end of the
-// launch), or, when there are too few to fill the SMs, the same rows with
-// their keys cut into about equal pieces; and the ranges of the decode
-// kernel's blocks.  The kernels behind it are launched for the most pieces
-// the arguments allow, and blocks without one return at once.
+// launch), or, when that ends sooner, the same rows with their keys cut into
+// about equal pieces; and the ranges of the decode kernel's blocks.  The kernels
+// behind it are launched for the most pieces the arguments allow (the tile kernel
+// of bf16 for a block per SM at most), and blocks without one return at once.
 #include <type_traits>
 
 #include "serving.h"
