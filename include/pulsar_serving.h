@@ -123,7 +123,9 @@ size_t pa_prompt_attend_workspace_size(int32_t B, int64_t N, int32_t hq, int32_t
  *  lse_opt        out [N][hq] float: natural-log sum of exp of the row's
  *                 scaled scores, or NULL.
  * Precision (bf16): the products q . k are exact and summed in fp32; the
- * softmax and all sums are fp32; the probabilities may be rounded to bf16
+ * softmax and all sums are fp32 (the tensor cores' drop what an addition cannot
+ * hold: at most 2^-9 of sum p |v|, however many keys; 3e-4 measured); the
+ * probabilities may be rounded to bf16
  * for the product with V (one rounding, half a step of 2^-7 relative; the
  * row sum is taken before it); one rounding of o.
  * A masked key adds nothing whatever its K and V hold (infinities and NaN

@@ -14,6 +14,7 @@ constexpr int kMaxGroup = 64;        // query heads per kv head: a tile holds at
 constexpr int kSms = 148;
 constexpr int kPlanTile = 128;       // keys per unit of planned work
 constexpr int kDecodeRows = 16;      // most rows per kv head of the decode kernel (one MMA's)
+constexpr int kFoldTiles = 2048;     // key tiles after which the tile kernel takes O out of its accumulator
 
 struct ScheduleArgs {
   const int32_t *q_len, *kv_len;
@@ -115,6 +116,7 @@ struct AttendArgs {
   int32_t* done;                  // [decode_ctas] arrivals at a cut (request, kv head)
   float* part_o;                  // [part_cap][hkv][tile_rows][d]
   float* part_lse;                // [part_cap][hkv][tile_rows]
+  float* fold;                    // [slots][2][256][d + 4] O so far of long pieces (tile kernel), or null: none is
   float* dec_o;                   // [2 * decode_ctas][16][d]
   float* dec_lse;                 // [2 * decode_ctas][16]
   uint64_t wait_limit_ns = 1000000000ull;

@@ -546,6 +546,8 @@ size_t plan_attend(AttendArgs& a, int64_t max_kv, void* ws) {
   const size_t parts = static_cast<size_t>(a.part_cap) * a.hkv * a.tile_rows;
   take(a.part_lse, parts);
   take(a.part_o, parts * a.d);
+  const bool folds = a.tiles && a.dtype == PA_BF16 && deep > kFoldTiles;
+  if (folds) take(a.fold, static_cast<size_t>(a.slots) * 2 * a.tile_rows * (a.d + 4));
   take(a.dec_lse, static_cast<size_t>(a.decode_ctas) * 2 * 16);
   take(a.dec_o, static_cast<size_t>(a.decode_ctas) * 2 * 16 * a.d);
   return off;

@@ -36,6 +36,14 @@
 // cap (7.0 ms before it sets in); 24 prompts of 1 to 4096 tokens 160 to 165 us; a
 // 64-token query over 128K keys 168 to 181 us with its plan and merge.
 //
+// A sum in TMEM loses the bits that one addition cannot hold, always towards
+// zero: o was 3e-4 too small over 512K keys in one accumulator, 1e-3 over 1M, 2 % over
+// 4M (equal weights).  So where a piece may be longer than kFoldTiles tiles, O goes
+// to a row in the workspace after every so many, added in fp32, and the next P V
+// starts anew (FOLD).  Calls whose tables or prompts cannot be that long have a
+// kernel without it: the same code cost them 2 to 4 % (ragged prompts 161 -> 167 us, one
+// 32K prompt 7.97 -> 8.18 ms, 32 mixed requests 97.4 -> 101.4).
+//
 // P is rounded to bf16 (half a step, 2^-8 of each probability; the row sum is taken
 // before it), as its product with V needs: a second product with the residual would
 // add half of the tensor pipe's work, and TMEM has no columns for it.
@@ -192,6 +200,18 @@ struct Item {
   int ctx;                         // position of the first new token (may be negative)
 };
 
+// Row `row` (of both warpgroups' 256) of the O so far of this block's pieces,
+// taken in turn: D sums and, behind them, the maximum that they are relative to.
+template <int D>
+__device__ __forceinline__ float* fold_row(const AttendArgs& a, int k, int row) {
+  return a.fold + ((static_cast<int64_t>(blockIdx.x) * 2 + (k & 1)) * 256 + row) * (D + 4);
+}
+// 2^((from - to) * scale): what a sum relative to the maximum `from` weighs in one
+// relative to `to`.
+__device__ __forceinline__ float reweight(float from, float to, float scale) {
+  return from == to ? 1.f : fast_exp2((from - to) * scale);
+}
+
 // The k-th piece of this block, once it is there; false: no more.
 __device__ __forceinline__ bool get_item(const SvBars* bars, int k, Item& it) {
   const int4 x = bars->work[k & 1].rows, y = bars->work[k & 1].keys, z = bars->work[k & 1].tiles;
@@ -213,7 +233,7 @@ __device__ __forceinline__ void put_item(SvBars* bars, int k, int tpt, const Pie
                                          2 * pc.b + two);
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool FOLD>
 __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                            const __grid_constant__ CUtensorMap tmK,
                                                            const __grid_constant__ CUtensorMap tmV,
@@ -372,9 +392,30 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
           sum += a0 + a1;
         }
         l_run = l_run * alpha + sum;
-        if (i > 0 && __any_sync(0xffffffffu, need)) {
-          // O was last written by the previous PV, which completed before this
-          // S (the commit signalling S covers every earlier MMA).
+        // O was last written by the previous PV, which completed before this S (the
+        // commit signalling S covers every earlier MMA).
+        if (FOLD && i > 0 && i % kFoldTiles == 0) {
+          // O to its row, with what is there; this tile's PV writes O anew
+          float* row = fold_row<D>(a, k, t * 128 + rl);
+          const float old = i > kFoldTiles ? reweight(row[D], m_run, C::SCALE) : 0.f;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t ov[32];
+            tmem_ld_x32(o_tmem + c, ov);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float4* d4 = reinterpret_cast<float4*>(row + c) + e;
+              float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (i > kFoldTiles) x = *d4;
+              x.x = x.x * old + __uint_as_float(ov[4 * e]) * alpha;
+              x.y = x.y * old + __uint_as_float(ov[4 * e + 1]) * alpha;
+              x.z = x.z * old + __uint_as_float(ov[4 * e + 2]) * alpha;
+              x.w = x.w * old + __uint_as_float(ov[4 * e + 3]) * alpha;
+              *d4 = x;
+            }
+          }
+          row[D] = m_run;
+        } else if (i > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t ov[32];
@@ -400,6 +441,10 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       const bool valid = rl < tpt * g && tok_t + rt < it.q_len;
       const int n_other = t == 0 ? it.nt1 : it.nt0;
       float w_own = 1.f, w_oth = 0.f;
+      // weights of what was folded, relative to O's
+      const bool folded = FOLD && (my > kFoldTiles || (!two && n_other > kFoldTiles));
+      float f_own = 0.f, f_oth = 0.f;
+      if (FOLD && my > kFoldTiles) f_own = reweight(fold_row<D>(a, k, t * 128 + rl)[D], m_run, C::SCALE);
       if (!two) {
         float (*ml)[2][128] = bars->ml[k & 1];
         ml[t][0][rl] = m_run;
@@ -409,6 +454,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
         if (!wait(&bars->ml_full[k & 1][t ^ 1], ph_ml >> (k & 1))) { ok = false; break; }
         ph_ml ^= 1u << (k & 1);
         const float m2 = ml[t ^ 1][0][rl], l2 = ml[t ^ 1][1][rl];
+        if (FOLD && n_other > kFoldTiles) f_oth = reweight(fold_row<D>(a, k, (t ^ 1) * 128 + rl)[D], m2, C::SCALE);
         const float m = fmaxf(m_run, m2);
         if (m != -INFINITY) {
           w_own = fast_exp2((m_run - m) * C::SCALE);
@@ -427,6 +473,8 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       const float lse = empty ? -INFINITY : ((m_run == -INFINITY ? 0.f : m_run * C::SCALE) + log2f(l_run)) * kLn2f;
       w_own *= inv;
       w_oth *= inv;
+      f_own *= w_own;
+      f_oth *= w_oth;
       const bool odd = *reinterpret_cast<volatile int*>(&bars->odd[k & 1]) == k + 1;
       const int64_t prow =
           (static_cast<int64_t>(it.part) * a.hkv + it.kvh) * a.tile_rows + (two ? t * tpt * g : 0) + rl;
@@ -439,12 +487,13 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
       }
       // What is read of shared memory is handed back by an ordinary arrival, which
       // orders the reads before whoever writes there next: before the output,
-      // whose stores it would wait for, unless there are notes to read behind it.
+      // whose stores it would wait for, unless there are notes, or rows that were
+      // folded, to read behind it.
       auto hand_back = [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->read[k & 1]);
       };
-      if (!odd) hand_back();
+      if (!odd && !folded) hand_back();
       // 32 columns at a time; with one row tile each warpgroup writes half of them
       const int c_lo = two ? 0 : t * (D / 2), c_hi = two ? D : c_lo + D / 2;
       // (below, four lanes write 64 bytes of a row: rows 8 x + lane / 4 of the warp)
@@ -469,6 +518,21 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
           tmem_ld_x32(o_oth + c, ov);
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] += __uint_as_float(ov[e]) * w_oth;
+        }
+        if (FOLD && folded) {
+          auto add = [&](int row, float w) {
+            const float4* s4 = reinterpret_cast<const float4*>(fold_row<D>(a, k, row) + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 x = s4[e];
+              v[4 * e] += x.x * w;
+              v[4 * e + 1] += x.y * w;
+              v[4 * e + 2] += x.z * w;
+              v[4 * e + 3] += x.w * w;
+            }
+          };
+          if (my > kFoldTiles) add(t * 128 + rl, f_own);
+          if (!two && n_other > kFoldTiles) add((t ^ 1) * 128 + rl, f_oth);
         }
         if (it.part >= 0) {
           if (valid) {
@@ -514,8 +578,8 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
             *x = __float2bfloat16_rn(__bfloat162float(*x) + add);
           }
         }
-        hand_back();
       }
+      if (odd || folded) hand_back();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_relaxed(&bars->done[k & 1]);   // O has been read
@@ -699,7 +763,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
                 if (jj < nt) {
                   if (!wait_one(&bars->p_full[t], next(ph_p, t))) { fail(5); ok = false; break; }
                   tc_fence_after();
-                  pv(t, st, jj > 0);
+                  pv(t, st, FOLD ? jj % kFoldTiles != 0 : jj > 0);
                   if (jj == nt - 1) mma_commit(&bars->o_final[t]);
                 }
                 if (t == 1) mma_commit(&bars->v_empty[st]);
@@ -726,7 +790,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
               if (jj == 0 && !wait_o()) { fail(12); ok = false; break; }
               if (!wait_one(&bars->p_full[t], next(ph_p, t))) { fail(5); ok = false; break; }
               tc_fence_after();
-              pv(t, st, i > 0);
+              pv(t, st, FOLD ? i % kFoldTiles != 0 : i > 0);
               if (jj + 2 >= n) mma_commit(&bars->o_final[t]);
               mma_commit(&bars->v_empty[st]);
               if (jj + 2 < n) {
@@ -777,7 +841,7 @@ __global__ void __launch_bounds__(384, 1) attend_tc_kernel(const __grid_constant
   }
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool FOLD>
 int launch_tc(const AttendArgs& a, cudaStream_t s) {
   using C = SvCfg<D>;
   const int g = a.hq / a.hkv;
@@ -799,11 +863,16 @@ int launch_tc(const AttendArgs& a, cudaStream_t s) {
       !rows_map(&mk, k, rows, a.hkv, D, a.ldk, 1, p.box_rows) ||
       !rows_map(&mv, v, rows, a.hkv, D, a.ldv, 1, p.box_rows))
     return PA_ERR_CUDA;
-  const int rc = allow_smem<attend_tc_kernel<D, PAGED>>(C::SMEM_BYTES);
+  const int rc = allow_smem<attend_tc_kernel<D, PAGED, FOLD>>(C::SMEM_BYTES);
   if (rc != PA_OK) return rc;
   const unsigned units = tile_blocks(a);
-  return launch_overlapped(attend_tc_kernel<D, PAGED>, dim3(units < kSms ? units : kSms), 384, C::SMEM_BYTES, s, mq, mk,
-                           mv, p);
+  return launch_overlapped(attend_tc_kernel<D, PAGED, FOLD>, dim3(units < kSms ? units : kSms), 384, C::SMEM_BYTES, s, mq,
+                           mk, mv, p);
+}
+template <int D>
+int launch_tc_for(const AttendArgs& a, cudaStream_t s) {
+  if (a.block_table) return a.fold ? launch_tc<D, true, true>(a, s) : launch_tc<D, true, false>(a, s);
+  return a.fold ? launch_tc<D, false, true>(a, s) : launch_tc<D, false, false>(a, s);
 }
 
 }  // namespace
@@ -829,9 +898,7 @@ bool rows_map(void* map, const void* base, int64_t rows, int heads, int d, int64
 }
 
 int launch_attend_tc(const AttendArgs& a, cudaStream_t s) {
-  if (a.block_table)
-    return a.d == 128 ? launch_tc<128, true>(a, s) : launch_tc<64, true>(a, s);
-  return a.d == 128 ? launch_tc<128, false>(a, s) : launch_tc<64, false>(a, s);
+  return a.d == 128 ? launch_tc_for<128>(a, s) : launch_tc_for<64>(a, s);
 }
 
 }  // namespace pa

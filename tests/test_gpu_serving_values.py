@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import serving_oracle as so
-from serving_cases import DTYPES, check_rows, paged_batch, randn
+from serving_cases import DTYPES, check_rows, half_step, paged_batch, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -124,6 +124,68 @@ def test_a_piece_may_last_longer_than_a_wait_between_tiles(S):
     assert torch.isfinite(o).all()
     keys = torch.arange(width * page - m + 1, width * page + 1, dtype=torch.float64)
     assert (lse.double().cpu() - keys.log()[:, None]).abs().max() <= 1e-4
+
+
+# What the tensor core adds in one accumulator: 2048 tiles of 128 keys, 16 keys to an
+# addition that drops the bits below its sum's last place, 2^-23 each at most.
+LONG_SUM = 2048 * 8 * 2.0 ** -23
+
+
+@pytest.mark.parametrize("kind,n_keys", [("one row tile", 2 ** 23), ("two row tiles", 2 ** 22), ("cut", 2 ** 27),
+                                         ("ragged", 2 ** 22 + 2048 * 128 + 1)])
+def test_sums_over_millions_of_keys_keep_their_size(S, kind, n_keys):
+    # equal scores: o is the mean of V over the keys, whatever their number.  (With
+    # 152 kv heads the keys are not cut.)
+    hq, hkv, m = {"one row tile": (152, 152, 20), "two row tiles": (608, 152, 64), "cut": (32, 8, 64),
+                  "ragged": (608, 152, 61)}[kind]
+    page, d = 1024, 64
+    width = -(-n_keys // page)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    k = torch.zeros((1, page, hkv, d), dtype=torch.bfloat16, device="cuda")
+    q = torch.ones((m, hq, d), dtype=torch.bfloat16, device="cuda")
+    args = (q, i32([0, m]), i32([n_keys]), torch.zeros((1, width), dtype=torch.int32, device="cuda"), k)
+    o, lse, ws = S.pa_paged_attend(*args, torch.ones_like(k), m)
+    assert ok(S, ws) == 0 and (o == 1).all()
+    assert (lse[-1].double() - np.log(n_keys)).abs().max() <= 1e-4
+    v = (randn(k.shape, torch.float32, 90).abs() + 0.5).bfloat16()
+    o, lse, ws = S.pa_paged_attend(*args, v, m)
+    assert ok(S, ws) == 0
+    # (whole pages but for less than 2^-11 of the keys)
+    want = v[0].double().mean(0).repeat_interleave(hq // hkv, 0)
+    off = (o[-1].double() - want) / want
+    assert off.abs().max() <= half_step(torch.bfloat16) + LONG_SUM + 2.0 ** -11
+    assert off.mean().abs() <= LONG_SUM
+
+
+def test_a_prompt_longer_than_one_sum(S):
+    # 600K tokens, more than two sums; scores grow along the sequence, so that the
+    # running maximum passes what was added before; then an infinite V near the front
+    n, hq, hkv, d = 600_000, 4, 1, 64
+    q, k = randn((n, hq, d), torch.bfloat16, 91), randn((n, hkv, d), torch.float32, 92)
+    k = (k * torch.linspace(0.2, 3.0, n, device="cuda")[:, None, None]).bfloat16()
+    v = (randn((n, hkv, d), torch.float32, 93).abs() + 0.5).bfloat16()
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    o, lse, ws = S.pa_prompt_attend(q, k, v, cu)
+    assert ok(S, ws) == 0 and torch.isfinite(o).all()
+    # (64 bits on the GPU: the rows have up to 600K keys)
+    kd, vd = k[:, 0].double(), v[:, 0].double()
+    half = half_step(torch.bfloat16)
+    for i in (0, 2047 * 128, 2048 * 128 - 1, 2048 * 128, 2048 * 128 + 64, 400_000, 2 * 2048 * 128 + 5, n - 1):
+        s = q[i].double() @ kd[:i + 1].T / d ** 0.5
+        z = torch.logsumexp(s, -1)
+        want = torch.exp(s - z[:, None]) @ vd[:i + 1]
+        # P rounded, o rounded, and the sum (V is positive: sum p |v| = o)
+        off = ((o[i].double() - want) / want).abs().max()
+        assert off <= 2 * half * (1 + half) + LONG_SUM, f"row {i}: {off:.2e}"
+        assert (lse[i].double() - z).abs().max() <= 1e-4, f"row {i}"
+    v2 = v.clone()
+    v2[1000, 0, 5] = float("inf")
+    o2, lse2, ws = S.pa_prompt_attend(q, k, v2, cu)
+    assert ok(S, ws) == 0 and torch.equal(lse2, lse)
+    assert not torch.isfinite(o2[1000:, :, 5]).any()
+    keep = torch.ones_like(o, dtype=torch.bool)
+    keep[1000:, :, 5] = False
+    assert torch.equal(o2[keep], o[keep])
 
 
 def spread_rows(n, count):

@@ -5,10 +5,10 @@ test_serving_sync_model.
 Every role has a vector clock.  An ordinary mbarrier arrival releases it (into
 the phase that the arrival counts for) and a wait acquires that phase's; a
 relaxed arrival, the completion of a copy and the commit of MMAs carry none.
-The locations are those in shared memory that roles read and write as ordinary
-memory and use again for a later piece: `work` (a piece as its roles see it),
-the notes of non-finite V (`first`, `odd`) and the exchanged maxima and sums
-(`ml`).  A write must come after all earlier reads and writes of the location
+The locations are those that roles read and write as ordinary memory and use
+again for a later piece: `work` (a piece as its roles see it), the notes of
+non-finite V (`first`, `odd`), the exchanged maxima and sums (`ml`), and the rows
+to which a long piece's O is folded (here with every tile).  A write must come after all earlier reads and writes of the location
 by other roles in the order that the clocks give, a read after its last write.
 """
 import heapq
@@ -50,6 +50,7 @@ class OrderModel(Model):
         self.hands_back, self.plant = hands_back, mutation
         self.work, self.notes = Slots(self, "work", 2), Slots(self, "notes", 2)
         self.ml = [Slots(self, f"ml{b}", 2) for b in (0, 1)]
+        self.fold = [Slots(self, f"fold{b}", 2) for b in (0, 1)]
         Bar = type(self.bars["q_full"])
         for i in (0, 1):
             self.bars[f"read{i}"] = Bar(f"read{i}", 8 if mutation == "issuer not counted" else 9)
@@ -112,8 +113,12 @@ class OrderModel(Model):
             b, k = int(bar[-1]), self.piece[self.role]
             self.saw(("work", b))
             self.saw(("notes", b))
-            if not self.item(k)["two"]:
-                self.saw((f"ml{b}", 1 - int(self.role[-1])))
+            it, t = self.item(k), int(self.role[-1])
+            if not it["two"]:
+                self.saw((f"ml{b}", 1 - t))
+            for u in (t,) if it["two"] else (0, 1):
+                if it["nt"][u]:
+                    self.saw((f"fold{self.fold_of(k)}", u))
             if self.hands_back:
                 if self.plant == "handed back relaxed":
                     self.bars[f"read{b}"].arrive(n)
@@ -121,7 +126,12 @@ class OrderModel(Model):
                     self.release(f"read{b}", n)
             self.bars[bar].arrive(n)          # relaxed
         else:
+            if bar.startswith("p_full"):
+                self.fold[self.fold_of(self.piece[self.role])][int(self.role[-1])] = True
             self.release(bar, n)
+
+    def fold_of(self, k):
+        return 0 if self.plant == "one row for all pieces" else k & 1
 
     def get(self, k, who):
         yield from super().get(k, who)
@@ -169,9 +179,10 @@ def test_every_reuse_of_shared_memory_is_ordered(seed):
     assert m.checked > len(m.pieces)
 
 
-@pytest.mark.parametrize("kw", [dict(hands_back=False), dict(mutation="handed back relaxed"), dict(mutation="issuer not counted")],
+@pytest.mark.parametrize("kw", [dict(hands_back=False), dict(mutation="handed back relaxed"), dict(mutation="issuer not counted"),
+                                dict(mutation="one row for all pieces")],
                          ids=lambda kw: str(*kw.values()))
 def test_planted_mistakes_are_caught(kw):
     for seed in range(10):
-        with pytest.raises(Fail, match="nothing orders"):
-            OrderModel(seed, pieces_of(seed) + [(2, True, 2, 0)] * 4, **kw).run()
+        with pytest.raises(Fail, match="nothing orders|not ordered behind"):
+            OrderModel(seed, pieces_of(seed) + [(2, True, 2, 0)] * 4 + [(4, False, 4, 0)] * 12, **kw).run()
