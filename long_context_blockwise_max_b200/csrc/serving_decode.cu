@@ -18,6 +18,11 @@
 // MMA rows 0-7 and residual in rows 8-15, at no extra MMA; with 9 to 16 rows
 // they are rounded to bf16.
 //
+// An accumulator of the MMA loses the bits that one addition cannot hold, always
+// towards zero (o 9e-3 too small over 1.8M keys in one warp, equal weights): where
+// a warp may have more keys of a pair than kFoldKeys, it adds its o to its part of
+// the merge memory after every so many and starts anew (FOLD, a kernel of its own).
+//
 // Rows whose keys lie in several blocks' ranges leave partial results in the
 // workspace; the last block to arrive merges them in block order, so results
 // do not depend on which block that is.
@@ -40,6 +45,7 @@ constexpr int kWarps = 4;
 constexpr int kKT = 32;      // keys per warp tile
 constexpr int kStages = 3;
 constexpr int kMergeAhead = 8;   // parts of a cut pair that are loaded together
+constexpr int kFoldKeys = kFoldTiles * kPlanTile;   // keys that an accumulator adds up at most
 static_assert(kWarps * kKT == kPlanTile, "a block's step is one planned key group");
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -117,7 +123,7 @@ struct Cursor {
   }
 };
 
-template <int D>
+template <int D, bool FOLD>
 __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __grid_constant__ CUtensorMap tmK,
                                                                        const __grid_constant__ CUtensorMap tmV,
                                                                        const __grid_constant__ AttendArgs a,
@@ -198,6 +204,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
   int rows = 0, ctx = 0;
   int lim0 = -1, lim1 = -1;
   bool pair = true;             // at most 8 rows: P as a high part and a residual
+  int since = 0;                // FOLD: tiles in o; whether there are more in the merge memory
+  bool folded = false;
   auto begin = [&]() {
     rows = cur.q * g;
     ctx = cur.kv - cur.q;
@@ -219,6 +227,41 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
     for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     m0 = m1 = -INFINITY;
     l0 = l1 = 0.f;
+    if (FOLD) {
+      since = 0;
+      folded = false;
+    }
+  };
+  // o so far, with what was folded before: to this warp's part of the merge memory
+  // (each thread its own elements of it), o being relative to the maxima m0, m1
+  auto put = [&]() {
+    float f0 = 0.f, f1 = 0.f;
+    if (FOLD && folded) {
+      const float a0 = red_m[warp * 16 + qi], a1 = red_m[warp * 16 + qi + 8];
+      f0 = a0 == m0 ? 1.f : fast_exp2((a0 - m0) * C::SCALE);
+      f1 = a1 == m1 ? 1.f : fast_exp2((a1 - m1) * C::SCALE);
+    }
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) {
+      float2 lo = make_float2(o[j][0], o[j][1]);
+      float2* r0 = reinterpret_cast<float2*>(red + (warp * 16 + qi) * D + 8 * j + qc);
+      if (pair) {
+        lo.x += o[j][2];
+        lo.y += o[j][3];
+      } else {
+        float2 hi = make_float2(o[j][2], o[j][3]);
+        float2* r1 = reinterpret_cast<float2*>(red + (warp * 16 + qi + 8) * D + 8 * j + qc);
+        if (FOLD && folded) hi = make_float2(r1->x * f1 + hi.x, r1->y * f1 + hi.y);
+        *r1 = hi;
+      }
+      if (FOLD && folded) lo = make_float2(r0->x * f0 + lo.x, r0->y * f0 + lo.y);
+      *r0 = lo;
+    }
+    __syncwarp();   // the old maxima have been read
+    if ((lane & 3) == 0) {
+      red_m[warp * 16 + qi] = m0;
+      red_m[warp * 16 + qi + 8] = m1;
+    }
   };
 
 #pragma unroll
@@ -340,6 +383,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
           mma_bf16(o[2 * cj], pf[k2], vb[0], vb[1]);
           mma_bf16(o[2 * cj + 1], pf[k2], vb[2], vb[3]);
         }
+      if (FOLD && ++since == kFoldKeys / kKT) {
+        put();
+        folded = true;
+        since = 0;
+        __syncwarp();   // its maxima are written
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+      }
     }
     __syncwarp();   // the stage is refilled by the next issue
     const bool item_end = cur.unit == cur.n_units - 1;
@@ -352,21 +403,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-#pragma unroll
-    for (int j = 0; j < D / 8; ++j) {
-      float2 lo = make_float2(o[j][0], o[j][1]);
-      if (pair) {
-        lo.x += o[j][2];
-        lo.y += o[j][3];
-      } else {
-        *reinterpret_cast<float2*>(red + (warp * 16 + qi + 8) * D + 8 * j + qc) = make_float2(o[j][2], o[j][3]);
-      }
-      *reinterpret_cast<float2*>(red + (warp * 16 + qi) * D + 8 * j + qc) = lo;
-    }
+    put();
     if ((lane & 3) == 0) {
-      red_m[warp * 16 + qi] = m0;
       red_l[warp * 16 + qi] = l0;
-      red_m[warp * 16 + qi + 8] = m1;
       red_l[warp * 16 + qi + 8] = l1;
     }
     __syncthreads();
@@ -501,11 +540,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_decode_kernel(const __g
   }
 }
 
-template <int D>
+template <int D, bool FOLD>
 int launch(const AttendArgs& a, cudaStream_t s) {
   constexpr int smem = DecCfg<D>::SMEM;
   static_assert(smem <= 232448, "shared memory of one block");
-  const int rc = allow_smem<attend_decode_kernel<D>>(smem);
+  const int rc = allow_smem<attend_decode_kernel<D, FOLD>>(smem);
   if (rc != PA_OK) return rc;
   // (an empty cache has no page to read: every box is out of range, and the
   // maps are made over q only to have an address)
@@ -515,14 +554,17 @@ int launch(const AttendArgs& a, cudaStream_t s) {
   if (!rows_map(&mk, a.n_slots > 0 ? a.k : a.q, rows, a.hkv, D, a.ldk, 1, box) ||
       !rows_map(&mv, a.n_slots > 0 ? a.v : a.q, rows, a.hkv, D, a.ldv, 1, box))
     return PA_ERR_CUDA;
-  return launch_overlapped(attend_decode_kernel<D>, dim3(a.decode_ctas), kWarps * 32, smem, s, mk, mv, a, box,
+  return launch_overlapped(attend_decode_kernel<D, FOLD>, dim3(a.decode_ctas), kWarps * 32, smem, s, mk, mv, a, box,
                            static_cast<int>(rows));
 }
 
 }  // namespace
 
 int launch_attend_decode(const AttendArgs& a, cudaStream_t s) {
-  return a.d == 128 ? launch<128>(a, s) : launch<64>(a, s);
+  // a warp has a quarter of a request's keys at most
+  const bool fold = static_cast<int64_t>(a.max_pages) * a.page_size / kWarps > kFoldKeys;
+  if (a.d == 128) return fold ? launch<128, true>(a, s) : launch<128, false>(a, s);
+  return fold ? launch<64, true>(a, s) : launch<64, false>(a, s);
 }
 
 }  // namespace pa

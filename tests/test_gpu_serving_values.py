@@ -132,12 +132,14 @@ LONG_SUM = 2048 * 8 * 2.0 ** -23
 
 
 @pytest.mark.parametrize("kind,n_keys", [("one row tile", 2 ** 23), ("two row tiles", 2 ** 22), ("cut", 2 ** 27),
-                                         ("ragged", 2 ** 22 + 2048 * 128 + 1)])
+                                         ("ragged", 2 ** 22 + 2048 * 128 + 1), ("one token", 2 ** 27),
+                                         ("one token, 16 rows", 2 ** 27), ("two tokens, 12 rows", 2 ** 26)])
 def test_sums_over_millions_of_keys_keep_their_size(S, kind, n_keys):
     # equal scores: o is the mean of V over the keys, whatever their number.  (With
     # 152 kv heads the keys are not cut.)
     hq, hkv, m = {"one row tile": (152, 152, 20), "two row tiles": (608, 152, 64), "cut": (32, 8, 64),
-                  "ragged": (608, 152, 61)}[kind]
+                  "ragged": (608, 152, 61), "one token": (8, 8, 1), "one token, 16 rows": (128, 8, 1),
+                  "two tokens, 12 rows": (48, 8, 2)}[kind]
     page, d = 1024, 64
     width = -(-n_keys // page)
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
