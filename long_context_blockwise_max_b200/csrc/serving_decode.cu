@@ -29,8 +29,8 @@
 //
 // HBM-bound when long: 16 tokens over 128K keys each, 32 / 8 heads of 128, 1226
 // to 1290 us (between boxes) for 8.59 GB = 6.66 to 7.0 TB/s, 1.02 to 1.07 of a copy's
-// rate.  Latency-bound when short: 8 tokens behind up to 1467 keys 13.2 us, of which
-// 7 are a block's own (table, copies and 32 keys' chain 2 us, parts and arrival
+// rate.  Latency-bound when short: 8 tokens behind up to 1467 keys 13.6 to 14.1 us, of
+// which 7 are a block's own (table, copies and 32 keys' chain 2 us, parts and arrival
 // 2 us, the last one's merge 1 us) and the rest the plan and two launches.
 #include "serving.h"
 #include "sm100.cuh"
