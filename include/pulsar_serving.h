@@ -53,7 +53,8 @@ size_t pa_paged_schedule_workspace_size(int32_t B);
  *  kv_len         [B] int32, tokens each request has in the cache.
  *  block_table    in/out: the first ceil(kv_len / page_size) entries of a
  *                 request are its pages; the pages it needs for its new
- *                 tokens are written behind them.
+ *                 tokens are written behind them.  Must not overlap the
+ *                 lengths or free_pages.
  *  free_pages     [n_free] int32: new pages are taken from its front, in
  *                 the order of the requests.
  *  cu_q           out [B + 1] int32: exclusive prefix sum of q_len.
@@ -93,6 +94,7 @@ size_t pa_paged_append_workspace_size(int64_t N);
  *  k_pages, v_pages  in/out [n_slots][hkv][d]: rows slots[i] receive token
  *                 i's rotated K and its V.  slots, k_pages and v_pages may be
  *                 NULL together: nothing is appended (v is then not read).
+ *                 They must not overlap one another or what the call reads.
  *  q_out          out [N][hq][d] dense: the rotated q.  May equal q when ldq
  *                 is hq * d.
  *  k_out_opt      out [N][hkv][d] dense: the rotated k, or NULL.  May equal k

@@ -159,6 +159,22 @@ def test_sums_over_millions_of_keys_keep_their_size(S, kind, n_keys):
     assert off.mean().abs() <= LONG_SUM
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1, 3], [700, 1, 2000]), ([40, 1, 200], [300, 900, 3000]), ([100], [9000]),
+                                            ([1, 2, 1], [0, 5, 129]), ([300, 20, 0, 7], [300, 20, 4, 500])])
+def test_a_wide_table_changes_no_result(S, d, q_lens, kv_lens):
+    # the same requests in a table with room for more than a million keys each: the
+    # kernels that can fold, with nothing to fold
+    c = paged_batch(q_lens, kv_lens, 16, 4, d, 16, torch.bfloat16, seed=d + len(q_lens))
+    run = lambda t: S.pa_paged_attend(c["q"], c["cu_q"], c["kv_len"], t, c["k_pages"], c["v_pages"], c["max_q"])
+    o0, lse0, ws = run(c["table"])
+    assert ok(S, ws) == 0
+    wide = torch.full((len(q_lens), 70_000), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    wide[:, :c["table"].shape[1]] = c["table"]
+    o, lse, ws2 = run(wide)
+    assert ok(S, ws2) == 0 and torch.equal(lse, lse0) and torch.equal(o, o0)
+
+
 def test_a_prompt_longer_than_one_sum(S):
     # 600K tokens, more than two sums; scores grow along the sequence, so that the
     # running maximum passes what was added before; then an infinite V near the front
