@@ -133,3 +133,52 @@ def test_other_threads_run_while_launches_wait(S):
         torch.cuda.synchronize()
         assert waited > 0.4, "no launch had to wait"
         assert max(gaps) < 0.2, f"another thread stood still for {max(gaps):.2f} of {waited:.2f} s"
+
+
+@pytest.mark.parametrize("captured", [False, True], ids=["eager", "captured"])
+def test_a_call_waits_for_what_another_stream_has_to_give(S, captured):
+    # q, the lengths and the pages come late from another stream; the calls' kernels,
+    # which are set up early, read them only then
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rn = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()
+    new = dict(x=rn(70, 12, 64), q_len=i32([1, 64, 5]), kv=i32([29, 136, 85]), kp=rn(40, 16, 2, 64), vp=rn(40, 16, 2, 64))
+    now = {k: torch.zeros_like(t) if t.dtype == torch.bfloat16 else i32([1, 1, 1]) for k, t in new.items()}
+    table, free = torch.arange(39, dtype=torch.int32, device="cuda").view(3, 13), i32(range(39))
+    other = torch.cuda.Stream()
+
+    def step(src):
+        cu, kv, pos, slots, _, w0 = S.pa_paged_schedule(src["q_len"], src["kv"], table, free, 16, 70)
+        q, _, w1 = S.pa_paged_append(src["x"][:, :8], src["x"][:, 8:10], src["x"][:, 10:], pos, slots, src["kp"], src["vp"],
+                                     rope_theta=1e4)
+        o, lse, w2 = S.pa_paged_attend(q, cu, kv, table, src["kp"], src["vp"], 64)
+        p, _, w3 = S.pa_prompt_attend(q, src["x"][:, 8:10], src["x"][:, 10:], cu)
+        return o, lse, p, slots, w0, w1, w2, w3
+
+    def late():
+        main = torch.cuda.current_stream()
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            torch.cuda._sleep(20_000_000)
+            for k in new:
+                now[k].copy_(new[k])
+        main.wait_stream(other)
+        return step(now)
+    want = step({k: t.clone() for k, t in new.items()})
+    again = {k: t.clone() for k, t in now.items()}
+    step(again)
+    torch.cuda.synchronize()
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = late()
+    for _ in range(2):
+        for k, t in now.items():
+            t.copy_(torch.zeros_like(t) if t.dtype == torch.bfloat16 else i32([1, 1, 1]))
+        if captured:
+            g.replay()
+        else:
+            got = late()
+        torch.cuda.synchronize()
+        assert all(S.pulsar.pa_workspace_status(w) == 0 for w in got[4:])
+        for a, b in zip(got[:4], want[:4]):
+            assert torch.equal(a, b)
